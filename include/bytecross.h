@@ -388,6 +388,225 @@ BC_API bc_status bc_batch_step(bc_batch* b, const int* tokens, bc_mode mode, dou
 BC_API bc_status bc_batch_trace(const bc_batch* b, int seq, int layer, bc_trace_kind kind, const void** ptr,
                                 int* count, int* stride);
 
+/* ------------------------------------------------------------------ ragged batches over an 8-bit cache */
+
+/* Operators for a batch of sequences of different lengths that share one
+ * paged cache of 8-bit keys and values.  One call of bc_block_tables plans a
+ * step (which pages each sequence gets, where each new token goes); per layer
+ * bc_kv8_append writes the new tokens and bc_kv8_attention attends over the
+ * cache; bc_kv8_gather reads tokens back (to hand a prefix to bc_kv_append);
+ * bc_logits_adjust applies penalties, biases and grammar masks to the logits.
+ * All five are asynchronous on `stream` (a cudaStream_t of the current
+ * device), allocate nothing and can be captured into a graph.  Every index
+ * that a kernel takes from device memory is checked against the sizes given
+ * here; what is outside is skipped as stated, never read or written.
+ *
+ * Cache pool of one layer: uint8 [n_pages][n_kv_heads][32 hd + 32], one block
+ * per page of 16 tokens and kv head:
+ *   key codes    [hd / 64][16 tokens][64 dims]
+ *   value codes  [hd / 4][4 groups of tokens][4 dims][4 tokens]
+ *   f32 key scale, f32 value scale, 24 unused bytes
+ * A key or value is its code times its block's scale.  Token t of a page is
+ * slot page * 16 + t of the pool.  A page needs no clearing before its first
+ * use; tokens of a page are written in order, from its token 0 on.
+ * head_dim is 64 or 128, the pool is 16-byte aligned, and
+ * n_pages * 16 <= 2^31 - 1. */
+
+/* Element types of queries, outputs, new keys and values, and logits. */
+typedef enum { BC_F32 = 0, BC_BF16 = 1 } bc_dtype;
+/* Code types of the 8-bit cache: floating point with 4 exponent and 3
+ * mantissa bits (largest value 448), or integers -127..127. */
+typedef enum { BC_KV8_E4M3 = 0, BC_KV8_INT8 = 1 } bc_kv8_type;
+
+/* Bytes of one layer's pool.  0 on bad sizes. */
+BC_API size_t bc_kv8_pool_bytes(int n_pages, int n_kv_heads, int head_dim);
+
+/* The plan of one step of a ragged batch, from the requests' lengths.
+ * Sequence b holds lens[b] tokens in the pages table[b][0 ..
+ * ceil(lens[b]/16)), and changes by delta[b]:
+ *   < 0  its last -delta tokens are dropped (all of them if it holds no
+ *        more), and the pages that hold none of its tokens any longer are
+ *        given back;
+ *   > 0  it takes delta new tokens and the pages they need;
+ *   0    nothing.
+ * The free pages are free_list[0 .. n_free) followed by the pages given back
+ * in this call (in order of sequence, then of page); pages are taken from the
+ * end of that list, in order of sequence.  A sequence that asks for tokens is
+ * refused, and keeps its length, if
+ *   lens + delta > 16 max_blocks, or
+ *   the delta of the sequences up to it (those refused so far by the line
+ *   above left out) add up to more than max_tokens, or
+ *   it needs pages, and the pages needed by the sequences up to it (those
+ *   refused by the two lines above left out) are more than the free ones.
+ * Lengths outside [0, 16 max_blocks] are taken as the nearest bound, a
+ * count n_free outside [0, n_pages] likewise.
+ * Written: the new entries of table (no others), free_list (the pages given
+ * back and not taken, behind the old ones), lens_out, n_free_out, q_start
+ * (the running sum of the new tokens; a refused sequence has none), and for
+ * new token i of q_start[batch], in order of sequence and position, slots[i]
+ * and positions[i]; both are -1 from there to max_tokens.
+ * lens_out may be lens and n_free_out may be n_free; no other buffers may
+ * overlap.
+ *   1 <= batch <= 2048; max_tokens >= 0 (then slots and positions may be
+ *   NULL if it is 0).
+ *   ticket: device word, zero before the first call, left zero; calls that
+ *   may overlap on the GPU need one each.
+ * Errors: BC_EINVAL, BC_ECUDA. */
+#define BC_RAGGED_MAX_BATCH 2048
+typedef struct {
+  int batch, max_blocks, n_pages, max_tokens;
+  const int* lens;       /* [batch] */
+  const int* delta;      /* [batch] */
+  int* table;            /* [batch][max_blocks] */
+  int* free_list;        /* [n_pages] */
+  const int* n_free;     /* [1] */
+  int* lens_out;         /* [batch] */
+  int* n_free_out;       /* [1] */
+  int* q_start;          /* [batch + 1] */
+  int* slots;            /* [max_tokens] */
+  int* positions;        /* [max_tokens] */
+  unsigned* ticket;      /* [1] */
+} bc_block_tables_args;
+BC_API bc_status bc_block_tables(const bc_block_tables_args* a, void* stream);
+
+/* Writes n_tokens keys and values into the pool, token i to slot slots[i]
+ * (slots outside the pool, -1 among them, are skipped).
+ *   k, v   device f32 or bf16 (dtype), token i's head h at k + i * k_stride +
+ *          h * hd elements (strides let both be columns of a fused
+ *          projection's rows); 16-byte aligned for f32, 8-byte for bf16, the
+ *          strides multiples of 4 elements and at least n_kv_heads * hd
+ * Tokens that go to one page in one call are neighbours in slots, in order
+ * (slots[i + 1] = slots[i] + 1); a slot or page that comes up again later in
+ * the same call leaves that page's contents unspecified.
+ * Per block and for keys and values apart, with m the largest |x| of the new
+ * tokens and Q the largest code (448 or 127):
+ *   s = max(s_old, max(m / Q, 2^-126)), or s_old if m = 0, where s_old is the
+ *   block's scale, or 0 if the call writes the page's token 0;
+ *   the code of x is x * (1 / s) rounded to the nearest code (ties to even),
+ *   and if s > s_old the codes of the page's earlier tokens are replaced by
+ *   those of their values under s.
+ * A call that writes a page's token 0 sets the codes behind its last token to
+ * zero.  If a new key (value) is infinite or NaN, the block's key (value)
+ * scale becomes NaN, and so does every attention that sees the block.
+ * Errors: BC_EINVAL, BC_ECUDA. */
+BC_API bc_status bc_kv8_append(const void* k, const void* v, bc_dtype dtype, long long k_stride, long long v_stride,
+                               const int* slots, int n_tokens, void* pool, bc_kv8_type type, int n_pages,
+                               int n_kv_heads, int head_dim, void* stream);
+
+/* Reads tokens back: k_out and v_out (f32 or bf16, [n_tokens][n_kv_heads][hd],
+ * 16-byte aligned) receive code times scale of slot slots[i]; a slot outside
+ * the pool gives zeros.  Any order, slots may repeat.
+ * Errors: BC_EINVAL, BC_ECUDA. */
+BC_API bc_status bc_kv8_gather(const void* pool, bc_kv8_type type, int n_pages, int n_kv_heads, int head_dim,
+                               const int* slots, int n_tokens, void* k_out, void* v_out, bc_dtype dtype,
+                               void* stream);
+
+/* Attention of a ragged batch over the 8-bit cache.  Sequence b has n =
+ * lens[b] cached tokens and the query rows q_start[b] .. q_start[b + 1) (one
+ * row, b, if q_start is NULL); its queries are its last tokens, so that query
+ * i of m stands at position p = n - m + i.  Query head j (of kv head j / group) attends
+ * to the tokens t with t <= p, t > p - window if window > 0, and t / 16 in
+ * its kv head's page list if there is one, with the logits
+ *   x = scale * q . k[t],  x = cap * tanh(x / cap) if cap > 0,
+ *   x = x - slopes[j] * (p - t) if slopes is given,
+ * and out = sum_t softmax(x)[t] v[t].  A row that sees no token is 0.
+ * Masked tokens and pages contribute nothing, whatever their bytes hold.
+ *   q        f32 or bf16 rows [n_kv_heads * group][hd], row r at q +
+ *            r * q_stride elements, 16-byte aligned, q_stride a multiple of 8
+ *   n_q      rows of q and out; rows outside [0, n_q) are not computed
+ *   out      dtype of q, [n_q][n_kv_heads * group][hd], 16-byte aligned; rows
+ *            that belong to no sequence are left as they are
+ *   max_q    bound of every sequence's queries, 1 <= max_q and
+ *            group * max_q <= 64, group <= 8; of a sequence with more only
+ *            the first max_q rows are computed
+ *   table    [batch][max_blocks]; an entry outside [0, n_pages) is a page
+ *            that is not there
+ *   pages, n_sel  optional page lists: [batch][n_kv_heads][max_sel] pages of
+ *            the sequence (0 .. ceil(n/16) - 1, ascending, each once), the
+ *            first n_sel[b] of each row used; others of a row are skipped
+ *   scratch  bc_kv8_attention_scratch_bytes(...) bytes, 256-byte aligned:
+ *            partial results, a status word and tickets; zero it before the
+ *            first call.  Calls that may overlap on the GPU need one each.
+ * Lengths outside [0, 16 max_blocks] are taken as the nearest bound.
+ * Deterministic for the same sizes and lengths.
+ * Errors: BC_EINVAL, BC_ENOMEM, BC_ECUDA. */
+typedef struct {
+  const void* q;
+  void* out;
+  bc_dtype dtype;
+  long long q_stride;
+  int n_q;
+  const void* pool;
+  bc_kv8_type type;
+  int n_pages, n_kv_heads, group, head_dim;
+  int batch, max_q, max_blocks, max_sel;
+  const int* lens;       /* [batch] */
+  const int* q_start;    /* [batch + 1] or NULL */
+  const int* table;      /* [batch][max_blocks] */
+  const int* pages;      /* [batch][n_kv_heads][max_sel] or NULL */
+  const int* n_sel;      /* [batch], with pages */
+  float scale;           /* of q . k; usually 1 / sqrt(head_dim) */
+  float cap;             /* 0: none */
+  int window;            /* 0: none */
+  const float* slopes;   /* [n_kv_heads * group] or NULL */
+  void* scratch;
+  size_t scratch_bytes;
+} bc_kv8_attention_args;
+BC_API size_t bc_kv8_attention_scratch_bytes(int batch, int n_kv_heads, int group, int max_q, int head_dim);
+BC_API bc_status bc_kv8_attention(const bc_kv8_attention_args* a, void* stream);
+
+/* Waits for `stream` and reads the status word of a bc_kv8_attention scratch:
+ * BC_ETIMEOUT if a bounded wait of a call since the last look gave up (its
+ * outputs then hold NaN), after which the scratch is usable again. */
+BC_API bc_status bc_kv8_attention_status(void* scratch, void* stream);
+
+/* Penalties, biases and masks on the logits of a batch: for row b and token
+ * id v, with x the logit, in this order
+ *   x / repetition[b] if x > 0, else x * repetition[b], if v is in the row's
+ *     history;
+ *   x - (frequency[b] * c + presence[b]) if v is c > 0 times in the row's
+ *     history from its prompt_len[b]-th token on;
+ *   x + the bias listed for v (of an id listed twice, the last);
+ *   -inf if the row has a mask and v's bit in it is 0.
+ * Arithmetic in f32, rounded once to the output's type.
+ *   logits, out  f32 or bf16 [batch] rows of vocab, strides in elements; out
+ *                may be logits (with the same stride), else they do not overlap
+ *   hist         token ids; row b's are hist[hist_start[b] .. hist_start[b + 1]),
+ *                or none if hist is NULL.  Ids outside [0, vocab) count for
+ *                nothing.
+ *   prompt_len   how many of them are its prompt (NULL: none)
+ *   repetition, frequency, presence   [batch], each NULL for no such penalty
+ *   bias_ids, bias_vals, bias_start   likewise ragged, or NULL
+ *   mask         bits, n_masks rows of ceil(vocab / 32) words: token v is bit
+ *                v % 32 of word v / 32; NULL for none
+ *   mask_row     [batch] the mask of each row, no mask if outside [0, n_masks);
+ *                NULL: row b has mask b
+ * n_hist and n_bias are the lengths of hist and bias_ids; starts outside
+ * [0, length] are taken as the nearest bound.
+ * Errors: BC_EINVAL, BC_ECUDA. */
+typedef struct {
+  const void* logits;
+  void* out;
+  bc_dtype dtype;
+  int batch, vocab;
+  long long stride, out_stride;
+  const int* hist;
+  const int* hist_start;     /* [batch + 1] */
+  const int* prompt_len;     /* [batch] or NULL */
+  int n_hist;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const int* bias_ids;
+  const float* bias_vals;
+  const int* bias_start;     /* [batch + 1] */
+  int n_bias;
+  const uint32_t* mask;
+  const int* mask_row;       /* [batch] or NULL */
+  int n_masks;
+} bc_logits_args;
+BC_API bc_status bc_logits_adjust(const bc_logits_args* a, void* stream);
+
 /* ------------------------------------------------------------------ byte account */
 
 /* Bytes of one decode step.  Paper form: the pages' byte account (README,
