@@ -10,39 +10,41 @@
 // Work split.  The pages of all (sequence, kv head) pairs, in that order, are
 // one line of units; it is cut into equal pieces, one per worker, whatever
 // the lengths are: a worker's piece may begin and end inside a sequence and
-// hold several.  A CTA (one per SM) has 8 warps; NT warps that take 8 or 16
-// query rows each form a worker and share its pages.  A worker reads its
-// pages through a ring in shared memory, filled by bulk copies (a block of a
-// page and head, scales included, is contiguous) 4 NT pages ahead, 32 blocks
-// per SM; the page numbers come from registers, 64 units ahead.
+// hold several.  A CTA (one per SM) has 16 warps; a warp takes 8 query rows,
+// and the NT warps that share a sequence's rows form a worker and share its
+// pages.  A worker reads its pages through a ring in shared memory, filled by
+// bulk copies (a block of a page and head, scales included, is contiguous)
+// 2 NT pages ahead, 32 blocks per SM; the page numbers come from registers,
+// 64 units ahead.
 // A segment that lies in one worker's piece goes straight to the output.
 // Pieces of a segment are merged in shared memory within a CTA, and through
 // the scratch between CTAs, by the last of them to finish (an atomic ticket
 // per pair, no spinning).  All merges run in a fixed order.
 //
-// Products on mma.sync m16n8k16 with f16 operands: both code types are exact
-// in f16.  8 or 16 rows would leave 7/8 of a tcgen05 tile empty.  A row of q
-// is scaled by a power of two so that its largest element is in [1/2, 1) and
-// split in two f16 numbers, q = hi + lo (22 bits; a bf16 q is exact in hi
-// down to 2^-24 of its largest element); the weights likewise.  With up to 8
-// rows the two parts are the upper and the lower half of one A operand; 16
-// rows (bf16 only) take the first part alone, 11 bits against the 8 of the
-// output.
+// Products on mma.sync m16n8k16 with f16 operands (both code types are exact
+// in f16), the cache as the A operand and the 8 rows as its 8 columns, so no
+// part of a tile is idle: S^T = K Q^T, then O^T = V^T P^T.  A tcgen05 tile
+// would be 7/8 empty.  A row of q is scaled by a power of two so that its
+// largest element is in [1/2, 1).  A bf16 q is exact in f16 (down to 2^-24 of
+// its largest element), and weights of 11 bits serve a bf16 output of 8; for
+// f32 both are split in two f16 numbers, hi + lo (22 bits), for twice the
+// products.
 // The key scale multiplies the logit.  The value scale v of a page enters the
-// weight's exponent, w = 2^(x + log2 v - mo + 8), with a second running
-// maximum mo of x + log2 v: the f16 weight is then relative to the largest
-// weight times scale seen, however far apart the scales are, and 8 more bits
-// lie above f16's subnormals.
+// weight, w = 2^(x + log2 v - mo + 4), with a second reference mo for x +
+// log2 v: the f16 weight is then relative to the largest weight times scale
+// seen, however far apart the scales are.  The references m and mo follow
+// the maxima only when one is passed by more than 2^8 (one vote a page): the
+// reductions over the lanes and the rescaling of o leave the usual path.
 //
-// Fragment order.  Lane (g, t) = (lane / 4, lane % 4).  Keys: dims are
-// contracted in the order in which a lane finds them, 64u + 16t + 4w + 0..3
-// for step 4u + w (A and B alike).  The score columns are tokens in such an
-// order, 4 (n / 2) + 2j + n % 2 for column n of block j, that lane t holds
-// tokens 4t .. 4t + 3 of row g; that is the A operand of the second product
-// whose B operand is one word (4 tokens of a dim) of the value codes, which
-// are stored in that order, and the output block 4v + j holds dims
-// 4 (8v + n) + j.  Every shared-memory read is 16 bytes a lane, 512
-// contiguous ones a warp.
+// Fragment order.  Lane (g, t) = (lane / 4, lane % 4).  Dims are contracted
+// in the order in which a lane finds them, 64u + 16t + 4w + 0..3 for step
+// 4u + w (A and B alike).  Row n of score block j is token 4 (n / 2) + 2j +
+// n % 2, so that after a transpose of 8 x 8 (movmatrix) lane (g, t) holds the
+// weights of tokens 4t .. 4t + 3 for query row g: the B operand of the second
+// product, whose A operand is one word (4 tokens of a dim) of the value
+// codes, stored in that order.  Output block (v, i) holds dims 4 (8v + g) +
+// 2i, + 2i + 1, so a lane ends with 4 neighbouring dims of rows 2t and 2t+1.
+// Every shared-memory read is 16 bytes a lane, without bank conflicts.
 #include "entry.h"
 #include "kv8.cuh"
 
@@ -51,15 +53,16 @@
 
 namespace bc {
 
-constexpr int kA8Warps = 8;
+constexpr int kA8Warps = 16;
 constexpr int kA8Threads = kA8Warps * 32;
-constexpr int kA8Stages = 32;       // blocks in flight per CTA
+constexpr int kRingLog2 = 1;
+constexpr int kA8Stages = kA8Warps << kRingLog2;   // blocks in flight per CTA
 constexpr int kA8MaxCtas = 160;     // CTAs the scratch provides for
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Attn8Args {
   bc_kv8_attention_args a;
-  int nt;                 // warps per worker
+  int nt, nt_log2;        // warps per worker
   int rows;               // group * max_q
   float* part;            // [grid][2][rows][HD + 4] partials between CTAs
   unsigned* tickets;      // [batch * n_kv_heads], zero between calls
@@ -71,6 +74,11 @@ __device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x,
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {          // scales are 0, NaN or at least 2^-126
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -92,8 +100,23 @@ __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// 2^x relative to a maximum that may still be -inf (nothing seen)
-__device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
+// D = A * B, 16 x 8 f32 accumulators, A two rows of words (a: row g, b: row
+// g + 8; k order as B's)
+__device__ __forceinline__ void mma_words(float* c, const uint32_t a[2], const uint32_t b[2], const uint32_t* q) {
+  const uint32_t x[4] = {a[0], b[0], a[1], b[1]};
+  mma_f16(c, x, q[0], q[1]);
+}
+
+// 8 x 8 f16 transpose over the warp
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// References below every logit: nothing seen yet.
+constexpr float kNoMax = -1e38f;
+constexpr float kSlack = 8.f, kLift = 4.f;   // w <= 2^(kSlack + kLift), within f16
 
 // What a sequence needs of the cache.
 struct Seq {
@@ -120,16 +143,16 @@ __device__ __forceinline__ Seq seq_of(const bc_kv8_attention_args& a, int n, int
   return s;
 }
 
-template <int HD, int TYPE, bool R16, bool MODS>
+template <int HD, int TYPE, bool SPLIT, bool MODS>
 __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constant__ Attn8Args ga) {
   constexpr int BLK = kv8_block_bytes(HD);
-  constexpr int ROWS = R16 ? 16 : 8;       // query rows per warp
-  constexpr int NR = R16 ? 2 : 1;          // rows per lane
+  constexpr int ROWS = 8;                  // query rows per warp
   constexpr int U = HD / 64, V4 = HD / 32;
   constexpr int SROW = HD + 4;             // a partial's row: o, then m, l, mo
   const bc_kv8_attention_args& a = ga.a;
   const int B = a.batch, H = a.n_kv_heads, G = a.group, NT = ga.nt;
-  const int GP = kA8Warps / NT, S = kA8Stages / GP;     // workers per CTA, ring stages per worker
+  const int GP = kA8Warps >> ga.nt_log2;                // workers per CTA
+  const int s_log2 = kRingLog2 + ga.nt_log2, S = 1 << s_log2;   // ring stages per worker
 
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* ring = smem;
@@ -143,7 +166,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   __shared__ int s_last[2];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int worker = warp / NT, wt = warp % NT;
+  const int worker = warp >> ga.nt_log2, wt = warp & (NT - 1);
   const uint32_t full0 = smem_addr(bars) + 8 * worker * S, empty0 = full0 + 8 * kA8Stages;
   if (tid < kA8Stages) {
     mbar_init(smem_addr(bars) + 8 * tid, 1);
@@ -277,12 +300,14 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     for (; issued < min(S, n_units); ++issued) issue(issued);
 
   // ---- the segment at hand
+  // Lane (g, t) loads row g of the warp's queries; scores, weights and
+  // outputs are of rows 2t and 2t + 1.
   int b = 0, h = 0, seg_begin = g0, seg_end = g0;
   int r0 = 0, seg_rows = 0;
-  uint32_t qa[4 * U][4];
-  float o[4 * V4][4];
-  float m[NR], l[NR], mo[NR], qs[NR], slope[NR];
-  int lo[NR], hi[NR];                         // positions the row sees
+  uint32_t qh[4 * U][2], ql[SPLIT ? 4 * U : 1][2];
+  float o[V4][2][4];
+  float m[2], l[2], mo[2], qs[2], slope[2];
+  int lo[2], hi[2];                           // positions the row sees
   int tile_lo = 0, tile_hi = 0;               // positions every row of the warp sees
   int any_lo = 0, any_hi = 0;                 // positions some row of the warp sees
   bool live = false, dead = false;
@@ -294,20 +319,15 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     seg_rows = min(s.own, a.max_q) * G;
     live = wt * ROWS < seg_rows;
     #pragma unroll
-    for (int i = 0; i < 4 * V4; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      m[r] = mo[r] = -INFINITY;
-      l[r] = 0.f;
-    }
-    if (!live) return;
+    for (int v = 0; v < V4; ++v)
+      #pragma unroll
+      for (int i = 0; i < 4; ++i) o[v][0][i] = o[v][1][i] = 0.f;
     int w_lo = 0, w_hi = INT32_MAX, s_lo = INT32_MAX, s_hi = -1;
     #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const int row = wt * ROWS + g + 8 * r, i = row / G, j = h * G + row % G;
-      const int src = r0 + i;
-      const bool ok = row < seg_rows && src >= 0 && src < a.n_q;
-      const int p = s.n - s.own + i;
+    for (int r = 0; r < 2; ++r) {
+      m[r] = mo[r] = kNoMax;
+      l[r] = 0.f;
+      const int row = wt * ROWS + 2 * t + r, p = s.n - s.own + row / G;
       lo[r] = 0;
       hi[r] = INT32_MAX;
       if (row < seg_rows) {
@@ -318,180 +338,203 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
         s_lo = min(s_lo, lo[r]);
         s_hi = max(s_hi, hi[r]);
       }
-      slope[r] = MODS && a.slopes && row < seg_rows ? a.slopes[j] : 0.f;
-      float x[U][16];
-      uint32_t top = 0;
-      #pragma unroll
-      for (int c = 0; c < U; ++c) {
-        #pragma unroll
-        for (int d = 0; d < 16; ++d) x[c][d] = 0.f;
-        if (ok) {
-          const size_t at = (size_t)src * a.q_stride + (size_t)j * HD + 64 * c + 16 * t;
-          if (a.dtype == BC_F32) {
-            #pragma unroll
-            for (int d = 0; d < 16; d += 4) {
-              const float4 y = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + d);
-              x[c][d] = y.x; x[c][d + 1] = y.y; x[c][d + 2] = y.z; x[c][d + 3] = y.w;
-            }
-          } else {
-            #pragma unroll
-            for (int d = 0; d < 16; d += 8) {
-              const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at + d);
-              const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-              #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                x[c][d + 2 * e] = bf16_lo(w[e]);
-                x[c][d + 2 * e + 1] = bf16_hi(w[e]);
-              }
-            }
-          }
-        }
-        #pragma unroll
-        for (int d = 0; d < 16; ++d) top = max(top, __float_as_uint(x[c][d]) & 0x7fffffffu);
-      }
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = (int)(top >> 23);                    // q 2^(126 - e) is below 1
-      const float f = e == 255 ? __uint_as_float(0x7fc00000u) : ldexpf(1.f, 126 - e);
-      qs[r] = ldexpf(MODS ? a.scale : a.scale * kLog2e, e - 126);
-      #pragma unroll
-      for (int c = 0; c < U; ++c)
-        #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float* y = x[c] + 4 * w;
-          if (R16) {
-            qa[4 * c + w][r] = pack_f16x2(y[0] * f, y[1] * f);
-            qa[4 * c + w][2 + r] = pack_f16x2(y[2] * f, y[3] * f);
-          } else {
-            split_f16(y[0] * f, y[1] * f, qa[4 * c + w][0], qa[4 * c + w][1]);
-            split_f16(y[2] * f, y[3] * f, qa[4 * c + w][2], qa[4 * c + w][3]);
-          }
-        }
+      slope[r] = MODS && a.slopes && row < seg_rows ? a.slopes[h * G + row % G] : 0.f;
     }
+    if (!live) return;
     tile_lo = __reduce_max_sync(0xffffffffu, w_lo);
     tile_hi = __reduce_min_sync(0xffffffffu, w_hi);
     any_lo = __reduce_min_sync(0xffffffffu, s_lo);
     any_hi = __reduce_max_sync(0xffffffffu, s_hi);
+
+    const int row = wt * ROWS + g, src = r0 + row / G;
+    const bool ok = row < seg_rows && src >= 0 && src < a.n_q;
+    const size_t at = (size_t)(ok ? src : 0) * a.q_stride + (size_t)(ok ? h * G + row % G : 0) * HD + 16 * t;
+    float x[U][16];
+    uint32_t top = 0;
+    #pragma unroll
+    for (int c = 0; c < U; ++c) {
+      #pragma unroll
+      for (int d = 0; d < 16; ++d) x[c][d] = 0.f;
+      if (ok) {
+        if (SPLIT) {
+          #pragma unroll
+          for (int d = 0; d < 16; d += 4) {
+            const float4 y = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + 64 * c + d);
+            x[c][d] = y.x; x[c][d + 1] = y.y; x[c][d + 2] = y.z; x[c][d + 3] = y.w;
+          }
+        } else {
+          #pragma unroll
+          for (int d = 0; d < 16; d += 8) {
+            const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at + 64 * c + d);
+            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[c][d + 2 * e] = bf16_lo(w[e]);
+              x[c][d + 2 * e + 1] = bf16_hi(w[e]);
+            }
+          }
+        }
+      }
+      #pragma unroll
+      for (int d = 0; d < 16; ++d) top = max(top, __float_as_uint(x[c][d]) & 0x7fffffffu);
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int e = (int)(top >> 23);                    // q 2^(126 - e) is below 1
+    const float f = e == 255 ? __uint_as_float(0x7fc00000u) : ldexpf(1.f, 126 - e);
+    const float back = ldexpf(MODS ? a.scale : a.scale * kLog2e, e - 126);
+    qs[0] = __shfl_sync(0xffffffffu, back, 8 * t);
+    qs[1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+    #pragma unroll
+    for (int c = 0; c < U; ++c)
+      #pragma unroll
+      for (int w = 0; w < 4; ++w)
+        #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float y0 = x[c][4 * w + 2 * i] * f, y1 = x[c][4 * w + 2 * i + 1] * f;
+          if (SPLIT) split_f16(y0, y1, qh[4 * c + w][i], ql[4 * c + w][i]);
+          else qh[4 * c + w][i] = pack_f16x2(y0, y1);
+        }
   };
 
   auto process = [&](const uint8_t* blk, int lp) {
     const float* sc = reinterpret_cast<const float*>(blk + 2 * kPage * HD);
-    const float ks = sc[0], lvs = log2f(sc[1]);
-    float c[2][4];
-    #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
-      const uint8_t* kp = blk + (4 * (g >> 1) + 2 * j + (g & 1)) * 64 + t * 16;
+    const float ks = sc[0], lvs = lg2(sc[1]);
+    float ca[4] = {0.f, 0.f, 0.f, 0.f}, cb[4] = {0.f, 0.f, 0.f, 0.f};
+    {
+      const uint8_t* kp = blk + (4 * (g >> 1) + (g & 1)) * 64 + t * 16;
       #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const uint4 w = *reinterpret_cast<const uint4*>(kp + u * (kPage * 64));
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        const uint4 x = *reinterpret_cast<const uint4*>(kp + u * (kPage * 64));
+        const uint4 y = *reinterpret_cast<const uint4*>(kp + u * (kPage * 64) + 128);
+        const uint32_t xx[4] = {x.x, x.y, x.z, x.w}, yy[4] = {y.x, y.y, y.z, y.w};
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint32_t b0, b1;
-          Kv8Code<TYPE>::decode(ww[i], b0, b1);
-          mma_f16(c[j], qa[4 * u + i], b0, b1);
+          uint32_t p[2], q[2];
+          Kv8Code<TYPE>::decode(xx[i], p[0], p[1]);
+          Kv8Code<TYPE>::decode(yy[i], q[0], q[1]);
+          mma_words(SPLIT || !(i & 1) ? ca : cb, p, q, qh[4 * u + i]);
+          if (SPLIT) mma_words(cb, p, q, ql[4 * u + i]);
         }
       }
     }
-    const int pos0 = lp * kPage;
+    // this lane's scores: rows 2t + r, tokens 4 (g / 2) + 2j + g % 2
+    const int pos0 = lp * kPage, pos = pos0 + 4 * (g >> 1) + (g & 1);
     const bool whole = pos0 >= tile_lo && pos0 + kPage - 1 <= tile_hi;
-    float w[NR][4];
-    bool rescale = false;
-    float ao[NR];
+    float c[2][2], y[2][2], thr[2];
     #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      float x[4];
-      if (R16) {
-        x[0] = c[0][2 * r]; x[1] = c[0][2 * r + 1]; x[2] = c[1][2 * r]; x[3] = c[1][2 * r + 1];
-      } else {
-        x[0] = c[0][0] + c[0][2]; x[1] = c[0][1] + c[0][3]; x[2] = c[1][0] + c[1][2]; x[3] = c[1][1] + c[1][3];
-      }
+    for (int r = 0; r < 2; ++r) {
       const float f = qs[r] * ks;
-      bool see[4];
       #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[j] *= f;
-        const int pos = pos0 + 4 * t + j;
+      for (int j = 0; j < 2; ++j) {
+        float x = (ca[2 * j + r] + cb[2 * j + r]) * f;
         if (MODS) {
-          if (a.cap > 0.f) x[j] = a.cap * tanhf(x[j] / a.cap);
+          if (a.cap > 0.f) x = a.cap * tanhf(x / a.cap);
           // a row that is not there has hi = INT32_MAX and no slope
-          if (a.slopes) x[j] -= slope[r] * (float)(hi[r] - pos);
-          x[j] *= kLog2e;
+          if (a.slopes) x -= slope[r] * (float)(hi[r] - (pos + 2 * j));
+          x *= kLog2e;
         }
-        see[j] = whole || (pos >= lo[r] && pos <= hi[r]);
-        if (!see[j]) x[j] = -INFINITY;
+        c[r][j] = x;
       }
-      float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float m_new = fmaxf(m[r], mx), m_use = finite_or_0(m_new);
-      const float mo_new = fmaxf(mo[r], mx + lvs), mo_use = finite_or_0(mo_new);
-      const float al = ex2(m[r] - m_use);
-      ao[r] = ex2(mo[r] - mo_use);
-      rescale |= mo_new > mo[r];
-      m[r] = m_new;
-      mo[r] = mo_new;
-      const float shift = lvs - mo_use + 8.f;
-      float sum = 0.f;
-      #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float p = ex2(x[j] - m_use);
-        w[r][j] = ex2(x[j] + shift);
-        if (!see[j]) p = w[r][j] = 0.f;          // whatever the scales are
-        sum += p;
-      }
-      l[r] = l[r] * al + sum;
+      thr[r] = fminf(kSlack, kSlack - lvs - (m[r] - mo[r]));
     }
-    if (__any_sync(0xffffffffu, rescale)) {
-      #pragma unroll
-      for (int i = 0; i < 4 * V4; ++i) {
-        o[i][0] *= ao[0];
-        o[i][1] *= ao[0];
-        o[i][2] *= ao[NR - 1];
-        o[i][3] *= ao[NR - 1];
-      }
-    }
-    uint32_t pa[4];
-    if (R16) {
-      pa[0] = pack_f16x2(w[0][0], w[0][1]);
-      pa[1] = pack_f16x2(w[NR - 1][0], w[NR - 1][1]);
-      pa[2] = pack_f16x2(w[0][2], w[0][3]);
-      pa[3] = pack_f16x2(w[NR - 1][2], w[NR - 1][3]);
-    } else {
-      split_f16(w[0][0], w[0][1], pa[0], pa[1]);
-      split_f16(w[0][2], w[0][3], pa[2], pa[3]);
-    }
-    // value codes of tokens that no row sees may be any bytes: zero them
-    uint32_t keep = 0xffffffffu;
     if (!whole) {
       #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int pos = pos0 + 4 * t + j;
-        if (pos < any_lo || pos > any_hi) keep &= ~(0xffu << (8 * j));
+      for (int r = 0; r < 2; ++r)
+        #pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (pos + 2 * j < lo[r] || pos + 2 * j > hi[r]) c[r][j] = -INFINITY;
+    }
+    #pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      y[r][0] = c[r][0] - m[r];
+      y[r][1] = c[r][1] - m[r];
+    }
+    if (__any_sync(0xffffffffu, fmaxf(y[0][0], y[0][1]) > thr[0] || fmaxf(y[1][0], y[1][1]) > thr[1])) {
+      float ao[2];
+      #pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float mx = fmaxf(c[r][0], c[r][1]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        const float m_new = fmaxf(m[r], mx), mo_new = fmaxf(mo[r], mx + lvs);
+        l[r] *= ex2(m[r] - m_new);
+        ao[r] = ex2(mo[r] - mo_new);
+        m[r] = m_new;
+        mo[r] = mo_new;
+        y[r][0] = c[r][0] - m_new;
+        y[r][1] = c[r][1] - m_new;
       }
+      #pragma unroll
+      for (int v = 0; v < V4; ++v)
+        #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          o[v][i][0] *= ao[0];
+          o[v][i][1] *= ao[1];
+          o[v][i][2] *= ao[0];
+          o[v][i][3] *= ao[1];
+        }
+    }
+    float w[2][2];
+    #pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      // the bound keeps 0 * f a 0; it is passed only where p is below 2^-96
+      const float f = ex2(fminf(lvs + (m[r] - mo[r]) + kLift, 100.f));
+      #pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float p = ex2(y[r][j]);
+        l[r] += p;
+        w[r][j] = p * f;
+      }
+    }
+    uint32_t keep = 0xffffffffu;
+    if (!whole) {
+      // masked tokens weigh nothing, whatever the scales are (a key scale
+      // that is not a number was replaced with the score)
+      #pragma unroll
+      for (int r = 0; r < 2; ++r)
+        #pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (c[r][j] == -INFINITY) w[r][j] = 0.f;
+      // value codes of tokens that no row sees may be any bytes: zero them
+      #pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (pos0 + 4 * t + j < any_lo || pos0 + 4 * t + j > any_hi) keep &= ~(0xffu << (8 * j));
+    }
+    uint32_t ph[2], pl[2];
+    #pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (SPLIT) {
+        split_f16(w[0][j], w[1][j], ph[j], pl[j]);
+        pl[j] = movm(pl[j]);
+      } else {
+        ph[j] = pack_f16x2(w[0][j], w[1][j]);
+      }
+      ph[j] = movm(ph[j]);
     }
     #pragma unroll
     for (int v = 0; v < V4; ++v) {
       const uint4 x = *reinterpret_cast<const uint4*>(blk + kPage * HD + (8 * v + g) * 64 + t * 16);
       const uint32_t ww[4] = {x.x & keep, x.y & keep, x.z & keep, x.w & keep};
       #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t b0, b1;
-        Kv8Code<TYPE>::decode(ww[j], b0, b1);
-        mma_f16(o[4 * v + j], pa, b0, b1);
+      for (int i = 0; i < 2; ++i) {
+        uint32_t p[2], q[2];
+        Kv8Code<TYPE>::decode(ww[2 * i], p[0], p[1]);
+        Kv8Code<TYPE>::decode(ww[2 * i + 1], q[0], q[1]);
+        mma_words(o[v][i], p, q, ph);
+        if (SPLIT) mma_words(o[v][i], p, q, pl);
       }
     }
   };
 
-  // out = o / l 2^(mo - m - 8); nothing seen: 0
+  // out = o / l 2^(mo - m - kLift); nothing seen: 0
   auto final_factor = [](float mm, float ll, float mmo) {
-    if (ll == 0.f) return 0.f;
-    return mmo == -INFINITY && ll == ll ? 0.f : exp2f(finite_or_0(mmo) - finite_or_0(mm) - 8.f) / ll;
+    return ll == 0.f ? 0.f : exp2f(mmo - mm - kLift) / ll;
   };
   auto put = [&](int row, int j, int d, float4 y) {       // 4 dims of query row `row`, head j
     const size_t at = ((size_t)row * H * G + j) * HD + d;
-    if (a.dtype == BC_F32) {
+    if (SPLIT) {
       *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = y;
     } else {
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
@@ -502,30 +545,24 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   auto flush = [&](float* dst) {
     if (!live) return;
     #pragma unroll
-    for (int r = 0; r < NR; ++r) {
+    for (int r = 0; r < 2; ++r) {
       float ll = l[r];
-      ll += __shfl_xor_sync(0xffffffffu, ll, 1);
-      ll += __shfl_xor_sync(0xffffffffu, ll, 2);
+      ll += __shfl_xor_sync(0xffffffffu, ll, 4);
+      ll += __shfl_xor_sync(0xffffffffu, ll, 8);
+      ll += __shfl_xor_sync(0xffffffffu, ll, 16);
       if (dead) ll = __uint_as_float(0x7fc00000u);
-      const int row = wt * ROWS + g + 8 * r;
+      const int row = wt * ROWS + 2 * t + r;
       const float f = final_factor(m[r], ll, mo[r]);
-      const int i = row / G, src = r0 + i;
+      const int src = r0 + row / G;
       const bool ok = row < seg_rows && src >= 0 && src < a.n_q;
       #pragma unroll
-      for (int v = 0; v < V4; ++v)
-        #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float y[4];
-          #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            y[j] = R16 ? o[4 * v + j][2 * r + half] : o[4 * v + j][half] + o[4 * v + j][2 + half];
-          const int d = 32 * v + 8 * t + 4 * half;
-          if (dst)
-            *reinterpret_cast<float4*>(dst + (size_t)row * SROW + d) = make_float4(y[0], y[1], y[2], y[3]);
-          else if (ok)
-            put(src, h * G + row % G, d, make_float4(y[0] * f, y[1] * f, y[2] * f, y[3] * f));
-        }
-      if (dst && t == 0) {
+      for (int v = 0; v < V4; ++v) {
+        const float4 y = make_float4(o[v][0][r], o[v][0][2 + r], o[v][1][r], o[v][1][2 + r]);
+        const int d = 4 * (8 * v + g);
+        if (dst) *reinterpret_cast<float4*>(dst + (size_t)row * SROW + d) = y;
+        else if (ok) put(src, h * G + row % G, d, make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
+      }
+      if (dst && g == 0) {
         float* ml = dst + (size_t)row * SROW + HD;
         ml[0] = m[r];
         ml[1] = ll;
@@ -550,14 +587,14 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     }
     const int lp = __shfl_sync(0xffffffffu, lg0, k - base);
     const int stage = k & (S - 1);
-    if (!dead && !mbar_wait(full0 + 8 * stage, (k / S) & 1)) dead = true;
+    if (!dead && !mbar_wait(full0 + 8 * stage, (k >> s_log2) & 1)) dead = true;
     dead = __any_sync(0xffffffffu, dead);
     if (live && !dead && lp >= 0) process(my_ring + (size_t)stage * BLK, lp);
     __syncwarp();
     if (NT > 1 && lane == 0) mbar_arrive(empty0 + 8 * stage);
     const int old = k - lag;                            // its stage is free again
     if (wt == 0 && old >= 0 && old + S < n_units) {
-      if (NT > 1 && !dead && !mbar_wait(empty0 + 8 * (old & (S - 1)), (old / S) & 1)) dead = true;
+      if (NT > 1 && !dead && !mbar_wait(empty0 + 8 * (old & (S - 1)), (old >> s_log2) & 1)) dead = true;
       dead = __any_sync(0xffffffffu, dead);
       if (!dead) {
         issue(old + S);
@@ -574,7 +611,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     // copies still in flight land before the ring is used again
     if (lane == 0) atomicOr(ga.status, 1u);
     if (wt == 0)
-      for (int k = max(0, issued - S); k < issued; ++k) mbar_wait(full0 + 8 * (k & (S - 1)), (k / S) & 1);
+      for (int k = max(0, issued - S); k < issued; ++k) mbar_wait(full0 + 8 * (k & (S - 1)), (k >> s_log2) & 1);
   }
   __syncthreads();
   if (tail) flush(tails + (size_t)worker * NT * ROWS * SROW);
@@ -583,100 +620,144 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   // ---- segments cut between workers of this CTA, or between CTAs
   // A cut segment's pieces here: the tail of the worker it begins in (or the
   // head of worker 0 if it began in another CTA), then the heads of the next.
-  int n_cut = 0, cut_b[2], cut_h[2], cut_first[2], cut_count[2];
-  for (int w = -1; w < GP; ++w) {
-    int sb, sh, s0, s1;
+  // Lane w + 1 looks at worker w's last segment, lane 0 at the CTA's first.
+  struct Cut {
+    int b, h, s0, s1, first, last, rows;
+    bool from_tail;
+  };
+  __shared__ Cut s_cut[kA8Warps + 1];
+  __shared__ int s_ncut, s_nout, s_out_cut[2];   // cuts; bit i: slot i's segment goes on in another CTA
+  if (warp == 0) {
+    const int w = lane - 1;
     const int e0 = (int)min((long long)c0 + (long long)max(w, 0) * per, (long long)c1);
     const int e1 = (int)min((long long)e0 + per, (long long)c1);
-    if (e0 >= e1) continue;
-    locate(w < 0 ? c0 : e1 - 1, sb, sh, s0, s1);
-    if (w < 0 ? s0 >= c0 : s0 < e0 || s1 <= e1) continue;
-    const int w_first = max(w, 0), w_last = min(GP - 1, (min(s1, c1) - 1 - c0) / per);
-    const bool here = s0 >= c0 && s1 <= c1;
-    const int rows = min(max(s_row[sb + 1] - s_row[sb], 0), a.max_q) * G;
-    const int slot = s0 < c0 ? 0 : 1;
-    float* part = ga.part + ((size_t)blockIdx.x * 2 + slot) * ga.rows * SROW;
-    for (int e = tid; e < rows * (HD / 4); e += kA8Threads) {
-      const int row = e / (HD / 4), d = e % (HD / 4) * 4;
-      auto piece = [&](int x) {
-        return (w >= 0 && x == w ? tails : heads) + ((size_t)x * NT * ROWS + row) * SROW;
-      };
-      float M = -INFINITY, MO = -INFINITY, L = 0.f;
-      for (int x = w_first; x <= w_last; ++x) {
-        M = fmaxf(M, piece(x)[HD]);
-        MO = fmaxf(MO, piece(x)[HD + 2]);
-      }
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int x = w_first; x <= w_last; ++x) {
-        const float* q = piece(x);
-        L += ex2(q[HD] - finite_or_0(M)) * q[HD + 1];
-        const float f = ex2(q[HD + 2] - finite_or_0(MO));
-        const float4 y = *reinterpret_cast<const float4*>(q + d);
-        acc.x += f * y.x; acc.y += f * y.y; acc.z += f * y.z; acc.w += f * y.w;
-      }
-      if (here) {
-        const int src = s_row[sb] + row / G;
-        const float f = final_factor(M, L, MO);
-        if (src >= 0 && src < a.n_q) put(src, sh * G + row % G, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
-      } else {
-        float* dst = part + (size_t)row * SROW;
-        *reinterpret_cast<float4*>(dst + d) = acc;
-        if (d == 0) *reinterpret_cast<float4*>(dst + HD) = make_float4(M, L, MO, 0.f);
-      }
+    Cut c;
+    bool cut = w < GP && e0 < e1;
+    if (cut) {
+      locate(w < 0 ? c0 : e1 - 1, c.b, c.h, c.s0, c.s1);
+      cut = w < 0 ? c.s0 < c0 : c.s0 >= e0 && c.s1 > e1;
+      c.first = max(w, 0);
+      c.last = min(GP - 1, (min(c.s1, c1) - 1 - c0) / per);
+      c.rows = min(max(s_row[c.b + 1] - s_row[c.b], 0), a.max_q) * G;
+      c.from_tail = w >= 0;
     }
-    if (!here) {
-      cut_b[slot] = sb;
-      cut_h[slot] = sh;
-      cut_first[slot] = s0 / per_cta;
-      cut_count[slot] = (s1 - 1) / per_cta - s0 / per_cta + 1;
-      n_cut |= 1 << slot;
+    const unsigned mask = __ballot_sync(0xffffffffu, cut);
+    const int at = __popc(mask & ((1u << lane) - 1));
+    const bool head_out = cut && c.s0 < c0, tail_out = cut && !head_out && c.s1 > c1;
+    if (cut) s_cut[at] = c;
+    if (head_out) s_out_cut[0] = at;
+    if (tail_out) s_out_cut[1] = at;
+    const unsigned ho = __ballot_sync(0xffffffffu, head_out), to = __ballot_sync(0xffffffffu, tail_out);
+    if (lane == 0) {
+      s_ncut = __popc(mask);
+      s_nout = (ho ? 1 : 0) | (to ? 2 : 0);
     }
   }
-  if (!n_cut) return;
+  __syncthreads();
+  constexpr int D4 = HD / 4;
+  const int per_seg = ga.rows * D4;
+  for (int e = tid; e < s_ncut * per_seg; e += kA8Threads) {
+    const Cut& c = s_cut[e / per_seg];
+    const int row = e % per_seg / D4, d = e % D4 * 4;
+    if (row >= c.rows) continue;
+    auto piece = [&](int x) {
+      return (c.from_tail && x == c.first ? tails : heads) + ((size_t)x * NT * ROWS + row) * SROW;
+    };
+    float M = kNoMax, MO = kNoMax, L = 0.f;
+    #pragma unroll 4
+    for (int x = c.first; x <= c.last; ++x) {
+      const float4 ml = *reinterpret_cast<const float4*>(piece(x) + HD);
+      M = fmaxf(M, ml.x);
+      MO = fmaxf(MO, ml.z);
+    }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    #pragma unroll 4
+    for (int x = c.first; x <= c.last; ++x) {
+      const float* q = piece(x);
+      const float4 ml = *reinterpret_cast<const float4*>(q + HD);
+      const float4 y = *reinterpret_cast<const float4*>(q + d);
+      L += ex2(ml.x - M) * ml.y;
+      const float f = ex2(ml.z - MO);
+      acc.x += f * y.x; acc.y += f * y.y; acc.z += f * y.z; acc.w += f * y.w;
+    }
+    if (c.s0 >= c0 && c.s1 <= c1) {
+      const int src = s_row[c.b] + row / G;
+      const float f = final_factor(M, L, MO);
+      if (src >= 0 && src < a.n_q)
+        put(src, c.h * G + row % G, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+    } else {
+      float* dst = ga.part + (((size_t)blockIdx.x * 2 + (c.s0 < c0 ? 0 : 1)) * ga.rows + row) * SROW;
+      *reinterpret_cast<float4*>(dst + d) = acc;
+      if (d == 0) *reinterpret_cast<float4*>(dst + HD) = make_float4(M, L, MO, 0.f);
+    }
+  }
+  if (!s_nout) return;
 
   // ---- the last CTA of a cut segment merges its partials
   __syncthreads();
   if (tid < 2) {
-    s_last[tid] = 0;
-    if (n_cut >> tid & 1) {
-      unsigned* ticket = ga.tickets + (size_t)cut_b[tid] * H + cut_h[tid];
+    bool last = false;
+    if (s_nout >> tid & 1) {
+      const Cut& c = s_cut[s_out_cut[tid]];
+      unsigned* ticket = ga.tickets + (size_t)c.b * H + c.h;
       unsigned prev;
       asm volatile("atom.add.acq_rel.gpu.u32 %0, [%1], 1;" : "=r"(prev) : "l"(ticket) : "memory");
-      s_last[tid] = prev == (unsigned)(cut_count[tid] - 1);
-      if (s_last[tid]) *ticket = 0u;
+      last = prev == (unsigned)((c.s1 - 1) / per_cta - c.s0 / per_cta);
+      if (last) *ticket = 0u;
     }
+    s_last[tid] = last;
   }
   __syncthreads();
+  float* s_fac = reinterpret_cast<float*>(ring);        // [rows][partials]
+  float* s_out = s_fac + ga.rows * kA8MaxCtas;          // [rows]
   #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if (!s_last[i]) continue;
-    const int sb = cut_b[i], n_c = cut_count[i];
-    const int rows = min(max(s_row[sb + 1] - s_row[sb], 0), a.max_q) * G;
+    const Cut& c = s_cut[s_out_cut[i]];
+    const int first = c.s0 / per_cta, n_c = (c.s1 - 1) / per_cta - first + 1;
     // partial of the x-th CTA: the segment begins in the first one
     auto piece = [&](int x, int row) {
-      return ga.part + (((size_t)cut_first[i] + x) * 2 + (x == 0 ? 1 : 0)) * ga.rows * SROW + (size_t)row * SROW;
+      return ga.part + (((size_t)(first + x) * 2 + (x == 0 ? 1 : 0)) * ga.rows + row) * SROW;
     };
-    for (int e = tid; e < rows * (HD / 4); e += kA8Threads) {
-      const int row = e / (HD / 4), d = e % (HD / 4) * 4;
-      float M = -INFINITY, MO = -INFINITY, L = 0.f;
-      for (int x = 0; x < n_c; ++x) {
-        const float4 ml = __ldcg(reinterpret_cast<const float4*>(piece(x, row) + HD));
-        M = fmaxf(M, ml.x);
-        MO = fmaxf(MO, ml.z);
+    __syncthreads();                                    // s_fac of the other segment is read
+    for (int row = warp; row < c.rows; row += kA8Warps) {
+      float M = kNoMax, MO = kNoMax, L = 0.f;
+      float4 ml[kA8MaxCtas / 32];
+      #pragma unroll
+      for (int j = 0; j < kA8MaxCtas / 32; ++j) {
+        ml[j] = make_float4(kNoMax, 0.f, kNoMax, 0.f);
+        if (32 * j + lane < n_c) ml[j] = __ldcg(reinterpret_cast<const float4*>(piece(32 * j + lane, row) + HD));
+        M = fmaxf(M, ml[j].x);
+        MO = fmaxf(MO, ml[j].z);
       }
+      #pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, o));
+      }
+      #pragma unroll
+      for (int j = 0; j < kA8MaxCtas / 32; ++j) {
+        L += ex2(ml[j].x - M) * ml[j].y;
+        if (32 * j + lane < n_c) s_fac[row * kA8MaxCtas + 32 * j + lane] = ex2(ml[j].z - MO);
+      }
+      #pragma unroll
+      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      if (lane == 0) s_out[row] = final_factor(M, L, MO);
+    }
+    __syncthreads();
+    for (int e = tid; e < c.rows * D4; e += kA8Threads) {
+      const int row = e / D4, d = e % D4 * 4;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      #pragma unroll 8
       for (int x = 0; x < n_c; ++x) {
-        const float* q = piece(x, row);
-        const float4 ml = __ldcg(reinterpret_cast<const float4*>(q + HD));
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(q + d));
-        L += ex2(ml.x - finite_or_0(M)) * ml.y;
-        const float f = ex2(ml.z - finite_or_0(MO));
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(piece(x, row) + d));
+        const float f = s_fac[row * kA8MaxCtas + x];
         acc.x += f * y.x; acc.y += f * y.y; acc.z += f * y.z; acc.w += f * y.w;
       }
-      const int src = s_row[sb] + row / G;
-      const float f = final_factor(M, L, MO);
+      const int src = s_row[c.b] + row / G;
+      const float f = s_out[row];
       if (src >= 0 && src < a.n_q)
-        put(src, cut_h[i] * G + row % G, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+        put(src, c.h * G + row % G, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
     }
   }
 }
@@ -702,10 +783,10 @@ static Attn8Layout attn8_layout(int batch, int H, int rows, int hd) {
   return y;
 }
 
-template <int HD, int TYPE, bool R16, bool MODS>
+template <int HD, int TYPE, bool SPLIT, bool MODS>
 static cudaError_t attn8_launch(const Attn8Args& g, int grid, cudaStream_t st) {
-  auto kern = k_kv8_attn<HD, TYPE, R16, MODS>;
-  const size_t fixed = (size_t)kA8Stages * kv8_block_bytes(HD) + 4ull * kA8Warps * (R16 ? 16 : 8) * (HD + 4) +
+  auto kern = k_kv8_attn<HD, TYPE, SPLIT, MODS>;
+  const size_t fixed = (size_t)kA8Stages * kv8_block_bytes(HD) + 4ull * kA8Warps * 8 * (HD + 4) +
                        16ull * kA8Stages;
   // once per device: the most that any batch needs
   static std::atomic<unsigned long long> ready{0};
@@ -759,11 +840,9 @@ extern "C" bc_status bc_kv8_attention(const bc_kv8_attention_args* a, void* stre
   // a window that reaches every token is none
   if (a->window >= (long long)a->max_blocks * kPage + 64) g.a.window = 0;
   g.rows = a->group * a->max_q;
-  // 8 rows a warp with both f16 parts of queries and weights; 16 rows with
-  // the first part alone where the output is bf16 and 8 rows are not enough
-  const bool r16 = !f32 && g.rows > 8;
-  g.nt = 1;
-  while (g.nt * (r16 ? 16 : 8) < g.rows) g.nt *= 2;
+  g.nt_log2 = 0;
+  while ((8 << g.nt_log2) < g.rows) ++g.nt_log2;
+  g.nt = 1 << g.nt_log2;
   const Attn8Layout y = attn8_layout(a->batch, a->n_kv_heads, g.rows, a->head_dim);
   char* sc = static_cast<char*>(a->scratch);
   g.status = reinterpret_cast<unsigned*>(sc);
@@ -777,7 +856,7 @@ extern "C" bc_status bc_kv8_attention(const bc_kv8_attention_args* a, void* stre
   const bool mods = a->cap > 0.f || a->slopes;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 #define A8M(HD, TY, R) (mods ? attn8_launch<HD, TY, R, true>(g, grid, st) : attn8_launch<HD, TY, R, false>(g, grid, st))
-#define A8R(HD, TY) (r16 ? A8M(HD, TY, true) : A8M(HD, TY, false))
+#define A8R(HD, TY) (f32 ? A8M(HD, TY, true) : A8M(HD, TY, false))
 #define A8T(HD) (a->type == BC_KV8_E4M3 ? A8R(HD, 0) : A8R(HD, 1))
   e = a->head_dim == 128 ? A8T(128) : A8T(64);
 #undef A8T
