@@ -157,7 +157,6 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* ring = smem;
   float* heads = reinterpret_cast<float*>(smem + kA8Stages * BLK);          // [GP][NT * ROWS][SROW]
-  float* tails = reinterpret_cast<float*>(ring);                            // the same, once the ring is idle
   uint64_t* bars = reinterpret_cast<uint64_t*>(heads + kA8Warps * ROWS * SROW);   // full[32], empty[32]
   int* s_cum = reinterpret_cast<int*>(bars + 2 * kA8Stages);                // [B + 1] running sum of the pages
   int* s_len = s_cum + B + 1;                                               // [B]
@@ -184,8 +183,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     if (b < B) {
       const int n = (int)min((long long)max(a.lens[b], 0), (long long)a.max_blocks * kPage);
       // bounds keep the differences inside an int whatever q_start holds
-      const int r0 = a.q_start ? clampi(a.q_start[b], -(1 << 29), 1 << 30) : b;
-      const int own = a.q_start ? clampi(a.q_start[b + 1], -(1 << 29), 1 << 30) - r0 : 1;
+      const int r0 = a.q_start ? clampi(a.q_start[b], -(1 << 28), 1 << 29) : b;
+      const int own = a.q_start ? clampi(a.q_start[b + 1], -(1 << 28), 1 << 29) - r0 : 1;
       s_len[b] = n;
       s_row[b] = r0;
       if (b == B - 1) s_row[B] = r0 + own;
@@ -248,56 +247,53 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   };
   auto seq_at = [&](int b) { return seq_of(a, s_len[b], s_row[b], s_row[b + 1] - s_row[b], b); };
 
-  // ---- page numbers: lane l holds those of units base + l and base + 32 + l
-  auto lookup = [&](int k, int& phys, int& logical) {
-    phys = logical = -1;
+  // ---- block numbers (page * H + h) and pages of the sequence: lane l holds
+  // those of units base + l and base + 32 + l
+  auto lookup = [&](int k, int& block, int& logical) {
+    block = logical = -1;
     const int u = g0 + k;
     if (u >= g1) return;
     int b, h, begin, end;
     locate(u, b, h, begin, end);
-    const int nblk = (s_len[b] + kPage - 1) / kPage;
     int lp;
     if (a.pages) {
       lp = a.pages[((size_t)b * H + h) * a.max_sel + (u - begin)];
-      if (lp < 0 || lp >= nblk) return;
+      if (lp < 0 || lp >= (s_len[b] + kPage - 1) / kPage) return;
     } else {
       lp = seq_at(b).lo + (u - begin);
     }
     const int p = a.table[(size_t)b * a.max_blocks + lp];
     if (p < 0 || p >= a.n_pages) return;
     logical = lp;
-    phys = p;
+    block = p * H + h;
   };
-  int base = 0, ph0, ph1, lg0, lg1;
-  lookup(lane, ph0, lg0);
-  lookup(32 + lane, ph1, lg1);
-  auto phys_of = [&](int k) { return __shfl_sync(0xffffffffu, k - base < 32 ? ph0 : ph1, (k - base) & 31); };
+  int base = -32, bl0 = 0, bl1 = 0, lg0 = 0, lg1 = 0;
+  #pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    bl0 = bl1;
+    lg0 = lg1;
+    lookup(32 * i + lane, bl1, lg1);
+  }
+  base = 0;
 
   const int n_units = g1 - g0;
-  const uint8_t* pool = static_cast<const uint8_t*>(a.pool);
   uint8_t* my_ring = ring + (size_t)worker * S * BLK;
-  int is_b, is_h = 0, is_begin, is_end = g0;      // the pair of the unit issued last
   auto issue = [&](int k) {                       // by the leader warp, all lanes
-    const int p = phys_of(k);
-    const int u = g0 + k;
-    if (u >= is_end) locate(u, is_b, is_h, is_begin, is_end);
+    const int block = __shfl_sync(0xffffffffu, k - base < 32 ? bl0 : bl1, (k - base) & 31);
     if (lane == 0) {
       const uint32_t bar = full0 + 8 * (k & (S - 1));
-      if (p >= 0) {
+      if (block >= 0) {
         mbar_arrive_expect_tx(bar, BLK);
         asm volatile(
             "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                smem_addr(my_ring + (size_t)(k & (S - 1)) * BLK)),
-            "l"(pool + ((size_t)p * H + is_h) * BLK), "r"(BLK), "r"(bar)
+                smem_addr(my_ring + (k & (S - 1)) * BLK)),
+            "l"(static_cast<const uint8_t*>(a.pool) + (size_t)block * BLK), "r"(BLK), "r"(bar)
             : "memory");
       } else {
         mbar_arrive(bar);                         // a page that is not there
       }
     }
   };
-  int issued = 0;
-  if (wt == 0)
-    for (; issued < min(S, n_units); ++issued) issue(issued);
 
   // ---- the segment at hand
   // Lane (g, t) loads row g of the warp's queries; scores, weights and
@@ -309,8 +305,9 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   float m[2], l[2], mo[2], qs[2], slope[2];
   int lo[2], hi[2];                           // positions the row sees
   int tile_lo = 0, tile_hi = 0;               // positions every row of the warp sees
-  int any_lo = 0, any_hi = 0;                 // positions some row of the warp sees
-  bool live = false, dead = false;
+  int any_lo = 0, any_hi = 0;                 // positions some row of the segment sees
+  bool live = false;
+  int gave_up = -1;                           // a wait ran out: the pages issued until then
 
   auto begin_segment = [&](int u) {
     locate(u, b, h, seg_begin, seg_end);
@@ -322,7 +319,9 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     for (int v = 0; v < V4; ++v)
       #pragma unroll
       for (int i = 0; i < 4; ++i) o[v][0][i] = o[v][1][i] = 0.f;
-    int w_lo = 0, w_hi = INT32_MAX, s_lo = INT32_MAX, s_hi = -1;
+    int w_lo = 0, w_hi = INT32_MAX;
+    any_hi = s.n - s.own + min(s.own, a.max_q) - 1;
+    any_lo = a.window > 0 ? s.n - s.own - a.window + 1 : 0;
     #pragma unroll
     for (int r = 0; r < 2; ++r) {
       m[r] = mo[r] = kNoMax;
@@ -335,16 +334,12 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
         lo[r] = a.window > 0 ? max(0, p - a.window + 1) : 0;
         w_lo = max(w_lo, lo[r]);
         w_hi = min(w_hi, hi[r]);
-        s_lo = min(s_lo, lo[r]);
-        s_hi = max(s_hi, hi[r]);
       }
       slope[r] = MODS && a.slopes && row < seg_rows ? a.slopes[h * G + row % G] : 0.f;
     }
     if (!live) return;
     tile_lo = __reduce_max_sync(0xffffffffu, w_lo);
     tile_hi = __reduce_min_sync(0xffffffffu, w_hi);
-    any_lo = __reduce_min_sync(0xffffffffu, s_lo);
-    any_hi = __reduce_max_sync(0xffffffffu, s_hi);
 
     const int row = wt * ROWS + g, src = r0 + row / G;
     const bool ok = row < seg_rows && src >= 0 && src < a.n_q;
@@ -397,7 +392,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
         }
   };
 
-  auto process = [&](const uint8_t* blk, int lp) {
+  auto process = [&](uint8_t* blk, int lp) {
     const float* sc = reinterpret_cast<const float*>(blk + 2 * kPage * HD);
     const float ks = sc[0], lvs = lg2(sc[1]);
     float ca[4] = {0.f, 0.f, 0.f, 0.f}, cb[4] = {0.f, 0.f, 0.f, 0.f};
@@ -488,7 +483,6 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
         w[r][j] = p * f;
       }
     }
-    uint32_t keep = 0xffffffffu;
     if (!whole) {
       // masked tokens weigh nothing, whatever the scales are (a key scale
       // that is not a number was replaced with the score)
@@ -498,9 +492,16 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
         for (int j = 0; j < 2; ++j)
           if (c[r][j] == -INFINITY) w[r][j] = 0.f;
       // value codes of tokens that no row sees may be any bytes: zero them
+      // where this lane reads them (the worker's other warps write the same)
+      uint32_t keep = 0xffffffffu;
       #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (pos0 + 4 * t + j < any_lo || pos0 + 4 * t + j > any_hi) keep &= ~(0xffu << (8 * j));
+      #pragma unroll 1
+      for (int v = 0; v < V4; ++v) {
+        uint4* x = reinterpret_cast<uint4*>(blk + kPage * HD + (8 * v + g) * 64 + t * 16);
+        *x = make_uint4(x->x & keep, x->y & keep, x->z & keep, x->w & keep);
+      }
     }
     uint32_t ph[2], pl[2];
     #pragma unroll
@@ -516,7 +517,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     #pragma unroll
     for (int v = 0; v < V4; ++v) {
       const uint4 x = *reinterpret_cast<const uint4*>(blk + kPage * HD + (8 * v + g) * 64 + t * 16);
-      const uint32_t ww[4] = {x.x & keep, x.y & keep, x.z & keep, x.w & keep};
+      const uint32_t ww[4] = {x.x, x.y, x.z, x.w};
       #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint32_t p[2], q[2];
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
       ll += __shfl_xor_sync(0xffffffffu, ll, 4);
       ll += __shfl_xor_sync(0xffffffffu, ll, 8);
       ll += __shfl_xor_sync(0xffffffffu, ll, 16);
-      if (dead) ll = __uint_as_float(0x7fc00000u);
+      if (gave_up >= 0) ll = __uint_as_float(0x7fc00000u);
       const int row = wt * ROWS + 2 * t + r;
       const float f = final_factor(m[r], ll, mo[r]);
       const int src = r0 + row / G;
@@ -572,49 +573,56 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   };
   float* my_head = heads + (size_t)worker * NT * ROWS * SROW;
 
+  // The ring is filled `lag` pages behind the one just read (other warps of
+  // the worker may still read that one).  Round k < 0 only fills.
   const int lag = NT == 1 ? 0 : 1;
-  bool tail = false;
-  for (int k = 0; k < n_units; ++k) {
-    if (g0 + k == seg_end) {
-      if (k > 0) flush(seg_begin < g0 ? my_head : nullptr);
-      begin_segment(g0 + k);
-    }
-    if (k == base + 32) {
-      base += 32;
-      ph0 = ph1;
-      lg0 = lg1;
-      lookup(base + 32 + lane, ph1, lg1);
-    }
-    const int lp = __shfl_sync(0xffffffffu, lg0, k - base);
-    const int stage = k & (S - 1);
-    if (!dead && !mbar_wait(full0 + 8 * stage, (k >> s_log2) & 1)) dead = true;
-    dead = __any_sync(0xffffffffu, dead);
-    if (live && !dead && lp >= 0) process(my_ring + (size_t)stage * BLK, lp);
-    __syncwarp();
-    if (NT > 1 && lane == 0) mbar_arrive(empty0 + 8 * stage);
-    const int old = k - lag;                            // its stage is free again
-    if (wt == 0 && old >= 0 && old + S < n_units) {
-      if (NT > 1 && !dead && !mbar_wait(empty0 + 8 * (old & (S - 1)), (old >> s_log2) & 1)) dead = true;
-      dead = __any_sync(0xffffffffu, dead);
-      if (!dead) {
-        issue(old + S);
-        issued = old + S + 1;
+  int k = lag - S;
+  #pragma unroll 1
+  for (;; ++k) {
+    if (k >= 0) {
+      if (k == n_units || g0 + k == seg_end) {
+        if (k > 0) {
+          float* dst = seg_begin < g0 ? my_head : nullptr;
+          if (k == n_units && seg_begin >= g0 && seg_end > g1) {
+            // the tail goes into the worker's own ring, which is idle now
+            if (NT > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + worker), "r"(32 * NT) : "memory");
+            dst = reinterpret_cast<float*>(my_ring);
+          }
+          flush(dst);
+        }
+        if (k == n_units) break;
+        begin_segment(g0 + k);
       }
+      if (k == base + 32) {
+        base += 32;
+        bl0 = bl1;
+        lg0 = lg1;
+        lookup(base + 32 + lane, bl1, lg1);
+      }
+      const int lp = __shfl_sync(0xffffffffu, lg0, k - base), stage = k & (S - 1);
+      if (gave_up < 0) {
+        const bool ok = mbar_wait(full0 + 8 * stage, (k >> s_log2) & 1);
+        if (!__all_sync(0xffffffffu, ok)) gave_up = min(n_units, k + S - lag);
+      }
+      if (live && gave_up < 0 && lp >= 0) process(my_ring + stage * BLK, lp);
+      __syncwarp();
+      if (NT > 1 && lane == 0) mbar_arrive(empty0 + 8 * stage);
+    }
+    const int next = k + S - lag;
+    if (wt == 0 && next < n_units && gave_up < 0) {
+      if (NT > 1 && next >= S) {
+        const bool ok = mbar_wait(empty0 + 8 * (next & (S - 1)), ((next >> s_log2) - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) gave_up = next;
+      }
+      if (gave_up < 0) issue(next);
     }
   }
-  if (n_units > 0) {
-    if (seg_begin < g0) flush(my_head);
-    else if (seg_end <= g1) flush(nullptr);
-    else tail = true;
-  }
-  if (dead) {
-    // copies still in flight land before the ring is used again
+  if (gave_up >= 0) {
     if (lane == 0) atomicOr(ga.status, 1u);
+    // copies still in flight land before the ring is used again
     if (wt == 0)
-      for (int k = max(0, issued - S); k < issued; ++k) mbar_wait(full0 + 8 * (k & (S - 1)), (k >> s_log2) & 1);
+      for (int i = max(0, gave_up - S); i < gave_up; ++i) mbar_wait(full0 + 8 * (i & (S - 1)), (i >> s_log2) & 1);
   }
-  __syncthreads();
-  if (tail) flush(tails + (size_t)worker * NT * ROWS * SROW);
   __syncthreads();
 
   // ---- segments cut between workers of this CTA, or between CTAs
@@ -661,7 +669,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     const int row = e % per_seg / D4, d = e % D4 * 4;
     if (row >= c.rows) continue;
     auto piece = [&](int x) {
-      return (c.from_tail && x == c.first ? tails : heads) + ((size_t)x * NT * ROWS + row) * SROW;
+      return (c.from_tail && x == c.first ? reinterpret_cast<const float*>(ring + (size_t)x * S * BLK)
+                                          : heads + (size_t)x * NT * ROWS * SROW) + (size_t)row * SROW;
     };
     float M = kNoMax, MO = kNoMax, L = 0.f;
     #pragma unroll 4
@@ -819,9 +828,11 @@ extern "C" bc_status bc_kv8_attention(const bc_kv8_attention_args* a, void* stre
   if (a->dtype != BC_F32 && a->dtype != BC_BF16) return entry_fail(BC_EINVAL, "%s: bad dtype %d", who, (int)a->dtype);
   if (a->type != BC_KV8_E4M3 && a->type != BC_KV8_INT8)
     return entry_fail(BC_EINVAL, "%s: bad code type %d", who, (int)a->type);
-  if (a->n_pages < 1 || a->n_pages > INT32_MAX / kPage || a->max_blocks < 1 || a->max_blocks > 1 << 26 ||
-      a->n_q < 0 || a->n_q > 1 << 30 || (a->pages && a->max_sel < 1))
+  if (a->n_pages < 1 || a->n_pages > INT32_MAX / kPage || a->max_blocks < 1 || a->max_blocks > 1 << 25 ||
+      a->n_q < 0 || a->n_q > 1 << 29 || (a->pages && a->max_sel < 1))
     return entry_fail(BC_EINVAL, "%s: bad page or row counts", who);
+  if ((long long)a->n_pages * a->n_kv_heads > INT32_MAX)
+    return entry_fail(BC_EINVAL, "%s: more than 2^31 - 1 blocks in the pool", who);
   if ((long long)a->batch * a->n_kv_heads * std::max(a->max_blocks, a->pages ? a->max_sel : 0) > INT32_MAX)
     return entry_fail(BC_EINVAL, "%s: more than 2^31 - 1 pages over all sequences and heads", who);
   if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->pool, 16))
