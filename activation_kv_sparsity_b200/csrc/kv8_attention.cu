@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   }
 
   const int total = T * H;
-  const int per = max(1, (int)(((long long)total + gridDim.x * GP - 1) / (gridDim.x * GP)));   // units per worker
+  const int per = max(1, (int)(((unsigned)total + gridDim.x * GP - 1) / (gridDim.x * GP)));   // units per worker
   const int per_cta = per * GP;
   const int c0 = (int)min((long long)blockIdx.x * per_cta, (long long)total);
   const int c1 = (int)min((long long)c0 + per_cta, (long long)total);
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
 
   // the pair (b, h) that unit u belongs to, and the units of that pair
   auto locate = [&](int u, int& b, int& h, int& begin, int& end) {
-    const int x = u / H;
+    const int x = (unsigned)u / (unsigned)H;
     int lo = 0, hi = B;                      // last b with s_cum[b] <= x
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -241,40 +241,40 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     }
     b = lo;
     const int cnt = s_cum[b + 1] - s_cum[b], base = s_cum[b] * H;
-    h = (u - base) / cnt;
+    h = (unsigned)(u - base) / (unsigned)cnt;
     begin = base + h * cnt;
     end = begin + cnt;
   };
   auto seq_at = [&](int b) { return seq_of(a, s_len[b], s_row[b], s_row[b + 1] - s_row[b], b); };
 
-  // ---- block numbers (page * H + h) and pages of the sequence: lane l holds
-  // those of units base + l and base + 32 + l
-  auto lookup = [&](int k, int& block, int& logical) {
-    block = logical = -1;
-    const int u = g0 + k;
-    if (u >= g1) return;
-    int b, h, begin, end;
-    locate(u, b, h, begin, end);
-    int lp;
-    if (a.pages) {
-      lp = a.pages[((size_t)b * H + h) * a.max_sel + (u - begin)];
-      if (lp < 0 || lp >= (s_len[b] + kPage - 1) / kPage) return;
-    } else {
-      lp = seq_at(b).lo + (u - begin);
-    }
-    const int p = a.table[(size_t)b * a.max_blocks + lp];
-    if (p < 0 || p >= a.n_pages) return;
-    logical = lp;
-    block = p * H + h;
+  // ---- pages of the cache: lane l holds those of units base + l and base +
+  // 32 + l.  A lookup only starts its loads; found() turns what came into the
+  // block number page * H + h and the page of the sequence, or -1 (not there).
+  struct Page {
+    int block, logical, h, count;      // block: the table's entry until found()
   };
-  int base = -32, bl0 = 0, bl1 = 0, lg0 = 0, lg1 = 0;
-  #pragma unroll 1
-  for (int i = 0; i < 2; ++i) {
-    bl0 = bl1;
-    lg0 = lg1;
-    lookup(32 * i + lane, bl1, lg1);
-  }
-  base = 0;
+  auto lookup = [&](int k) {
+    Page p = {-1, -1, 0, 0};
+    const int u = g0 + k;
+    if (u >= g1) return p;
+    int b, begin, end;
+    locate(u, b, p.h, begin, end);
+    p.count = (s_len[b] + kPage - 1) / kPage;
+    if (a.pages) {
+      p.logical = a.pages[((size_t)b * H + p.h) * a.max_sel + (u - begin)];
+      if (p.logical < 0 || p.logical >= p.count) return p;
+    } else {
+      p.logical = seq_at(b).lo + (u - begin);
+    }
+    p.block = a.table[(size_t)b * a.max_blocks + p.logical];
+    return p;
+  };
+  auto found = [&](Page p, int& block, int& logical) {
+    const bool ok = p.block >= 0 && p.block < a.n_pages;
+    block = ok ? p.block * H + p.h : -1;
+    logical = ok ? p.logical : -1;
+  };
+  int base = 0, bl0 = -1, bl1 = -1, lg0 = -1, lg1 = -1;
 
   const int n_units = g1 - g0;
   uint8_t* my_ring = ring + (size_t)worker * S * BLK;
@@ -309,6 +309,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   bool live = false;
   int gave_up = -1;                           // a wait ran out: the pages issued until then
 
+  uint4 raw[SPLIT ? 4 * U : 2 * U];           // the query row as loaded
+  // takes up the segment of unit u and starts to load its queries
   auto begin_segment = [&](int u) {
     locate(u, b, h, seg_begin, seg_end);
     const Seq s = seq_at(b);
@@ -344,29 +346,35 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     const int row = wt * ROWS + g, src = r0 + row / G;
     const bool ok = row < seg_rows && src >= 0 && src < a.n_q;
     const size_t at = (size_t)(ok ? src : 0) * a.q_stride + (size_t)(ok ? h * G + row % G : 0) * HD + 16 * t;
+    #pragma unroll
+    for (int c = 0; c < U; ++c)
+      #pragma unroll
+      for (int i = 0; i < (SPLIT ? 4 : 2); ++i) {
+        const size_t e = at + 64 * c + (SPLIT ? 4 : 8) * i;
+        raw[(SPLIT ? 4 : 2) * c + i] =
+            !ok ? make_uint4(0, 0, 0, 0)
+                : SPLIT ? *reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + e)
+                        : *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + e);
+      }
+  };
+  // turns the loaded queries into operands
+  auto take_queries = [&]() {
+    if (!live) return;
     float x[U][16];
     uint32_t top = 0;
     #pragma unroll
     for (int c = 0; c < U; ++c) {
       #pragma unroll
-      for (int d = 0; d < 16; ++d) x[c][d] = 0.f;
-      if (ok) {
-        if (SPLIT) {
-          #pragma unroll
-          for (int d = 0; d < 16; d += 4) {
-            const float4 y = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + 64 * c + d);
-            x[c][d] = y.x; x[c][d + 1] = y.y; x[c][d + 2] = y.z; x[c][d + 3] = y.w;
-          }
-        } else {
-          #pragma unroll
-          for (int d = 0; d < 16; d += 8) {
-            const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at + 64 * c + d);
-            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-            #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              x[c][d + 2 * e] = bf16_lo(w[e]);
-              x[c][d + 2 * e + 1] = bf16_hi(w[e]);
-            }
+      for (int i = 0; i < (SPLIT ? 4 : 2); ++i) {
+        const uint4 y = raw[(SPLIT ? 4 : 2) * c + i];
+        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (SPLIT) {
+            x[c][4 * i + e] = __uint_as_float(w[e]);
+          } else {
+            x[c][8 * i + 2 * e] = bf16_lo(w[e]);
+            x[c][8 * i + 2 * e + 1] = bf16_hi(w[e]);
           }
         }
       }
@@ -573,41 +581,93 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   };
   float* my_head = heads + (size_t)worker * NT * ROWS * SROW;
 
-  // The ring is filled `lag` pages behind the one just read (other warps of
-  // the worker may still read that one).  Round k < 0 only fills.
-  const int lag = NT == 1 ? 0 : 1;
-  int k = lag - S;
-  #pragma unroll 1
-  for (;; ++k) {
-    if (k >= 0) {
-      if (k == n_units || g0 + k == seg_end) {
-        if (k > 0) {
-          float* dst = seg_begin < g0 ? my_head : nullptr;
-          if (k == n_units && seg_begin >= g0 && seg_end > g1) {
-            // the tail goes into the worker's own ring, which is idle now
-            if (NT > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + worker), "r"(32 * NT) : "memory");
-            dst = reinterpret_cast<float*>(my_ring);
-          }
-          flush(dst);
-        }
-        if (k == n_units) break;
-        begin_segment(g0 + k);
+  // Segments cut between workers of this CTA, or between CTAs.  A cut
+  // segment's pieces here: the tail of the worker it begins in (or the head
+  // of worker 0 if it began in another CTA), then the heads of the next.
+  // Lane w + 1 looks at worker w's last segment, lane 0 at the CTA's first,
+  // while the first pages are on their way.
+  struct Cut {
+    int b, h, s0, s1, first, last, rows;
+    bool from_tail;
+  };
+  __shared__ Cut s_cut[kA8Warps + 1];
+  __shared__ int s_ncut, s_nout, s_out_cut[2];   // cuts; bit i: slot i's segment goes on in another CTA
+  auto find_cuts = [&]() {
+    if (warp == kA8Warps - 1) {
+      const int w = lane - 1;
+      const int e0 = (int)min((long long)c0 + (long long)max(w, 0) * per, (long long)c1);
+      const int e1 = (int)min((long long)e0 + per, (long long)c1);
+      Cut c;
+      bool cut = w < GP && e0 < e1;
+      if (cut) {
+        locate(w < 0 ? c0 : e1 - 1, c.b, c.h, c.s0, c.s1);
+        cut = w < 0 ? c.s0 < c0 : c.s0 >= e0 && c.s1 > e1;
+        c.first = max(w, 0);
+        c.last = min(GP - 1, (min(c.s1, c1) - 1 - c0) / per);
+        c.rows = min(max(s_row[c.b + 1] - s_row[c.b], 0), a.max_q) * G;
+        c.from_tail = w >= 0;
       }
-      if (k == base + 32) {
-        base += 32;
-        bl0 = bl1;
-        lg0 = lg1;
-        lookup(base + 32 + lane, bl1, lg1);
+      const unsigned mask = __ballot_sync(0xffffffffu, cut);
+      const int at = __popc(mask & ((1u << lane) - 1));
+      const bool head_out = cut && c.s0 < c0, tail_out = cut && !head_out && c.s1 > c1;
+      if (cut) s_cut[at] = c;
+      if (head_out) s_out_cut[0] = at;
+      if (tail_out) s_out_cut[1] = at;
+      const unsigned ho = __ballot_sync(0xffffffffu, head_out), to = __ballot_sync(0xffffffffu, tail_out);
+      if (lane == 0) {
+        s_ncut = __popc(mask);
+        s_nout = (ho ? 1 : 0) | (to ? 2 : 0);
       }
-      const int lp = __shfl_sync(0xffffffffu, lg0, k - base), stage = k & (S - 1);
-      if (gave_up < 0) {
-        const bool ok = mbar_wait(full0 + 8 * stage, (k >> s_log2) & 1);
-        if (!__all_sync(0xffffffffu, ok)) gave_up = min(n_units, k + S - lag);
-      }
-      if (live && gave_up < 0 && lp >= 0) process(my_ring + stage * BLK, lp);
-      __syncwarp();
-      if (NT > 1 && lane == 0) mbar_arrive(empty0 + 8 * stage);
     }
+  };
+
+  // The ring is filled `lag` pages behind the one just read (other warps of
+  // the worker may still read that one).
+  const int lag = NT == 1 ? 0 : 1;
+  if (n_units > 0) begin_segment(g0);
+  {
+    const Page p0 = lookup(lane), p1 = n_units > 32 ? lookup(32 + lane) : Page{-1, -1, 0, 0};
+    found(p0, bl0, lg0);
+    found(p1, bl1, lg1);
+  }
+  if (wt == 0) {
+    #pragma unroll 1
+    for (int i = 0; i < min(S - lag, n_units); ++i) issue(i);
+  }
+  take_queries();
+  find_cuts();
+  Page coming = {-1, -1, 0, 0};
+  #pragma unroll 1
+  for (int k = 0;; ++k) {
+    if (k == n_units || g0 + k == seg_end) {
+      if (k > 0) {
+        float* dst = seg_begin < g0 ? my_head : nullptr;
+        if (k == n_units && seg_begin >= g0 && seg_end > g1) {
+          // the tail goes into the worker's own ring, which is idle now
+          if (NT > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + worker), "r"(32 * NT) : "memory");
+          dst = reinterpret_cast<float*>(my_ring);
+        }
+        flush(dst);
+      }
+      if (k == n_units) break;
+      begin_segment(g0 + k);
+      take_queries();
+    }
+    if ((k & 31) == 0 && k > 0) {
+      base = k;
+      bl0 = bl1;
+      lg0 = lg1;
+      coming = lookup(k + 32 + lane);
+    }
+    if ((k & 31) == 16 && k > 16) found(coming, bl1, lg1);      // the ring is at most 16 pages ahead
+    const int lp = __shfl_sync(0xffffffffu, lg0, k & 31), stage = k & (S - 1);
+    if (gave_up < 0) {
+      const bool ok = mbar_wait(full0 + 8 * stage, (k >> s_log2) & 1);
+      if (!__all_sync(0xffffffffu, ok)) gave_up = min(n_units, k + S - lag);
+    }
+    if (live && gave_up < 0 && lp >= 0) process(my_ring + stage * BLK, lp);
+    __syncwarp();
+    if (NT > 1 && lane == 0) mbar_arrive(empty0 + 8 * stage);
     const int next = k + S - lag;
     if (wt == 0 && next < n_units && gave_up < 0) {
       if (NT > 1 && next >= S) {
@@ -625,43 +685,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   }
   __syncthreads();
 
-  // ---- segments cut between workers of this CTA, or between CTAs
-  // A cut segment's pieces here: the tail of the worker it begins in (or the
-  // head of worker 0 if it began in another CTA), then the heads of the next.
-  // Lane w + 1 looks at worker w's last segment, lane 0 at the CTA's first.
-  struct Cut {
-    int b, h, s0, s1, first, last, rows;
-    bool from_tail;
-  };
-  __shared__ Cut s_cut[kA8Warps + 1];
-  __shared__ int s_ncut, s_nout, s_out_cut[2];   // cuts; bit i: slot i's segment goes on in another CTA
-  if (warp == 0) {
-    const int w = lane - 1;
-    const int e0 = (int)min((long long)c0 + (long long)max(w, 0) * per, (long long)c1);
-    const int e1 = (int)min((long long)e0 + per, (long long)c1);
-    Cut c;
-    bool cut = w < GP && e0 < e1;
-    if (cut) {
-      locate(w < 0 ? c0 : e1 - 1, c.b, c.h, c.s0, c.s1);
-      cut = w < 0 ? c.s0 < c0 : c.s0 >= e0 && c.s1 > e1;
-      c.first = max(w, 0);
-      c.last = min(GP - 1, (min(c.s1, c1) - 1 - c0) / per);
-      c.rows = min(max(s_row[c.b + 1] - s_row[c.b], 0), a.max_q) * G;
-      c.from_tail = w >= 0;
-    }
-    const unsigned mask = __ballot_sync(0xffffffffu, cut);
-    const int at = __popc(mask & ((1u << lane) - 1));
-    const bool head_out = cut && c.s0 < c0, tail_out = cut && !head_out && c.s1 > c1;
-    if (cut) s_cut[at] = c;
-    if (head_out) s_out_cut[0] = at;
-    if (tail_out) s_out_cut[1] = at;
-    const unsigned ho = __ballot_sync(0xffffffffu, head_out), to = __ballot_sync(0xffffffffu, tail_out);
-    if (lane == 0) {
-      s_ncut = __popc(mask);
-      s_nout = (ho ? 1 : 0) | (to ? 2 : 0);
-    }
-  }
-  __syncthreads();
+  // ---- merge the pieces of cut segments
   constexpr int D4 = HD / 4;
   const int per_seg = ga.rows * D4;
   for (int e = tid; e < s_ncut * per_seg; e += kA8Threads) {
