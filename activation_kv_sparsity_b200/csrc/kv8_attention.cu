@@ -278,6 +278,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
 
   const int n_units = g1 - g0;
   uint8_t* my_ring = ring + (size_t)worker * S * BLK;
+  uint64_t stream;                                // the cache is read once: first to leave L2
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(stream));
   auto issue = [&](int k) {                       // by the leader warp, all lanes
     const int block = __shfl_sync(0xffffffffu, k - base < 32 ? bl0 : bl1, (k - base) & 31);
     if (lane == 0) {
@@ -285,9 +287,10 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
       if (block >= 0) {
         mbar_arrive_expect_tx(bar, BLK);
         asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], "
+            "%4;" ::"r"(
                 smem_addr(my_ring + (k & (S - 1)) * BLK)),
-            "l"(static_cast<const uint8_t*>(a.pool) + (size_t)block * BLK), "r"(BLK), "r"(bar)
+            "l"(static_cast<const uint8_t*>(a.pool) + (size_t)block * BLK), "r"(BLK), "r"(bar), "l"(stream)
             : "memory");
       } else {
         mbar_arrive(bar);                         // a page that is not there
