@@ -53,10 +53,8 @@
 
 namespace bc {
 
-constexpr int kA8Warps = 16;
-constexpr int kA8Threads = kA8Warps * 32;
-constexpr int kRingLog2 = 1;
-constexpr int kA8Stages = kA8Warps << kRingLog2;   // blocks in flight per CTA
+constexpr int kA8Warps = 16, kA8Threads = kA8Warps * 32;
+constexpr int kA8Stages = 2 * kA8Warps;   // blocks in flight per CTA
 constexpr int kA8MaxCtas = 160;     // CTAs the scratch provides for
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -114,6 +112,26 @@ __device__ __forceinline__ uint32_t movm(uint32_t x) {
   return y;
 }
 
+// cap * tanh(x / cap).  With bf16 outputs from the fast exponential and
+// reciprocal, 1 - 2 / (1 + e^2t) with an error of 2^-23 or so, and for
+// |t| < 0.1, where that would be relative to more than the result, from
+// t - t^3 / 3 + 2 t^5 / 15 - 17 t^7 / 315 (next term below 10^-9 t).
+template <bool PRECISE>
+__device__ __forceinline__ float cap_logit(float x, float cap, float inv_cap) {
+  if (PRECISE) return cap * tanhf(x / cap);
+  const float t = x * inv_cap, u = t * t;
+  float q;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.f + ex2(2.f * kLog2e * t)));
+  const float p = x * fmaf(u, fmaf(u, fmaf(u, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+  return u < 0.01f ? p : fmaf(-2.f * cap, q, cap);
+}
+
+// A segment as its flush and its masks need it.
+struct Segment {
+  int h, begin, r0, rows;    // kv head, first unit, first query row, rows
+  int first, last;           // positions of its first and last query
+};
+
 // References below every logit: nothing seen yet.
 constexpr float kNoMax = -1e38f;
 constexpr float kSlack = 8.f, kLift = 4.f;   // w <= 2^(kSlack + kLift), within f16
@@ -143,6 +161,8 @@ __device__ __forceinline__ Seq seq_of(const bc_kv8_attention_args& a, int n, int
   return s;
 }
 
+// SPLIT: f32 queries and outputs (hi + lo operands); else bf16.  MODS: a cap
+// or slopes.
 template <int HD, int TYPE, bool SPLIT, bool MODS>
 __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constant__ Attn8Args ga) {
   constexpr int BLK = kv8_block_bytes(HD);
@@ -152,12 +172,12 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   const bc_kv8_attention_args& a = ga.a;
   const int B = a.batch, H = a.n_kv_heads, G = a.group, NT = ga.nt;
   const int GP = kA8Warps >> ga.nt_log2;                // workers per CTA
-  const int s_log2 = kRingLog2 + ga.nt_log2, S = 1 << s_log2;   // ring stages per worker
+  const int s_log2 = 1 + ga.nt_log2, S = 1 << s_log2;   // ring stages per worker
 
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* ring = smem;
   float* heads = reinterpret_cast<float*>(smem + kA8Stages * BLK);          // [GP][NT * ROWS][SROW]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(heads + kA8Warps * ROWS * SROW);   // full[32], empty[32]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(heads + kA8Warps * ROWS * SROW);   // full, then empty
   int* s_cum = reinterpret_cast<int*>(bars + 2 * kA8Stages);                // [B + 1] running sum of the pages
   int* s_len = s_cum + B + 1;                                               // [B]
   int* s_row = s_len + B;                                                   // [B + 1] first query rows
@@ -250,29 +270,28 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   // ---- pages of the cache: lane l holds those of units base + l and base +
   // 32 + l.  A lookup only starts its loads; found() turns what came into the
   // block number page * H + h and the page of the sequence, or -1 (not there).
-  struct Page {
-    int block, logical, h, count;      // block: the table's entry until found()
-  };
-  auto lookup = [&](int k) {
-    Page p = {-1, -1, 0, 0};
+  auto lookup = [&](int k, int& entry, int& logical) {
+    entry = logical = -1;
     const int u = g0 + k;
-    if (u >= g1) return p;
-    int b, begin, end;
-    locate(u, b, p.h, begin, end);
-    p.count = (s_len[b] + kPage - 1) / kPage;
+    if (u >= g1) return;
+    int b, h, begin, end;
+    locate(u, b, h, begin, end);
     if (a.pages) {
-      p.logical = a.pages[((size_t)b * H + p.h) * a.max_sel + (u - begin)];
-      if (p.logical < 0 || p.logical >= p.count) return p;
+      logical = a.pages[((size_t)b * H + h) * a.max_sel + (u - begin)];
+      if (logical < 0 || logical >= (s_len[b] + kPage - 1) / kPage) return;
     } else {
-      p.logical = seq_at(b).lo + (u - begin);
+      logical = seq_at(b).lo + (u - begin);
     }
-    p.block = a.table[(size_t)b * a.max_blocks + p.logical];
-    return p;
+    entry = a.table[(size_t)b * a.max_blocks + logical];
   };
-  auto found = [&](Page p, int& block, int& logical) {
-    const bool ok = p.block >= 0 && p.block < a.n_pages;
-    block = ok ? p.block * H + p.h : -1;
-    logical = ok ? p.logical : -1;
+  auto found = [&](int k, int& block, int& logical) {
+    int b, h, begin, end;
+    if (block >= 0 && block < a.n_pages) {
+      locate(g0 + k, b, h, begin, end);
+      block = block * H + h;
+    } else {
+      block = logical = -1;
+    }
   };
   int base = 0, bl0 = -1, bl1 = -1, lg0 = -1, lg1 = -1;
 
@@ -299,91 +318,82 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   };
 
   // ---- the segment at hand
-  // Lane (g, t) loads row g of the warp's queries; scores, weights and
+  // Lane (g, t) loads row g of each of the warp's tiles; scores, weights and
   // outputs are of rows 2t and 2t + 1.
-  int b = 0, h = 0, seg_begin = g0, seg_end = g0;
-  int r0 = 0, seg_rows = 0;
+  __shared__ Segment s_seg[kA8Warps];
+  Segment* my_seg = s_seg + warp;
+  int seg_end = g0;
   uint32_t qh[4 * U][2], ql[SPLIT ? 4 * U : 1][2];
   float o[V4][2][4];
   float m[2], l[2], mo[2], qs[2], slope[2];
-  int lo[2], hi[2];                           // positions the row sees
+  int at[2];                              // the row's position (rows that are not there: INT32_MAX)
   int tile_lo = 0, tile_hi = 0;               // positions every row of the warp sees
-  int any_lo = 0, any_hi = 0;                 // positions some row of the segment sees
   bool live = false;
   int gave_up = -1;                           // a wait ran out: the pages issued until then
 
-  uint4 raw[SPLIT ? 4 * U : 2 * U];           // the query row as loaded
+  constexpr int NRAW = SPLIT ? 4 * U : 2 * U;
+  uint4 raw[NRAW];                        // query rows as loaded
   // takes up the segment of unit u and starts to load its queries
   auto begin_segment = [&](int u) {
-    locate(u, b, h, seg_begin, seg_end);
+    int b, h, begin;
+    locate(u, b, h, begin, seg_end);
     const Seq s = seq_at(b);
-    r0 = s.r0;
-    seg_rows = min(s.own, a.max_q) * G;
+    const int seg_rows = min(s.own, a.max_q) * G, first = s.n - s.own;
     live = wt * ROWS < seg_rows;
+    if (lane == 0) *my_seg = Segment{h, begin, s.r0, seg_rows, first, first + min(s.own, a.max_q) - 1};
+    __syncwarp();
     #pragma unroll
     for (int v = 0; v < V4; ++v)
       #pragma unroll
       for (int i = 0; i < 4; ++i) o[v][0][i] = o[v][1][i] = 0.f;
     int w_lo = 0, w_hi = INT32_MAX;
-    any_hi = s.n - s.own + min(s.own, a.max_q) - 1;
-    any_lo = a.window > 0 ? s.n - s.own - a.window + 1 : 0;
     #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      m[r] = mo[r] = kNoMax;
-      l[r] = 0.f;
-      const int row = wt * ROWS + 2 * t + r, p = s.n - s.own + row / G;
-      lo[r] = 0;
-      hi[r] = INT32_MAX;
+    for (int i = 0; i < 2; ++i) {
+      m[i] = mo[i] = kNoMax;
+      l[i] = 0.f;
+      const int row = wt * ROWS + 2 * t + i;
+      at[i] = INT32_MAX;
       if (row < seg_rows) {
-        hi[r] = p;
-        lo[r] = a.window > 0 ? max(0, p - a.window + 1) : 0;
-        w_lo = max(w_lo, lo[r]);
-        w_hi = min(w_hi, hi[r]);
+        at[i] = first + row / G;
+        if (a.window > 0) w_lo = max(w_lo, at[i] - a.window + 1);
+        w_hi = min(w_hi, at[i]);
       }
-      slope[r] = MODS && a.slopes && row < seg_rows ? a.slopes[h * G + row % G] : 0.f;
+      slope[i] = MODS && a.slopes && row < seg_rows ? a.slopes[h * G + row % G] : 0.f;
     }
     if (!live) return;
     tile_lo = __reduce_max_sync(0xffffffffu, w_lo);
     tile_hi = __reduce_min_sync(0xffffffffu, w_hi);
-
-    const int row = wt * ROWS + g, src = r0 + row / G;
+    const int row = wt * ROWS + g, src = s.r0 + row / G;
     const bool ok = row < seg_rows && src >= 0 && src < a.n_q;
-    const size_t at = (size_t)(ok ? src : 0) * a.q_stride + (size_t)(ok ? h * G + row % G : 0) * HD + 16 * t;
+    const size_t e0 = (size_t)(ok ? src : 0) * a.q_stride + (size_t)(ok ? h * G + row % G : 0) * HD + 16 * t;
     #pragma unroll
-    for (int c = 0; c < U; ++c)
-      #pragma unroll
-      for (int i = 0; i < (SPLIT ? 4 : 2); ++i) {
-        const size_t e = at + 64 * c + (SPLIT ? 4 : 8) * i;
-        raw[(SPLIT ? 4 : 2) * c + i] =
-            !ok ? make_uint4(0, 0, 0, 0)
-                : SPLIT ? *reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + e)
-                        : *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + e);
-      }
+    for (int i = 0; i < NRAW; ++i) {
+      const size_t e = e0 + (SPLIT ? 64 * (i / 4) + 4 * (i % 4) : 64 * (i / 2) + 8 * (i % 2));
+      raw[i] = !ok ? make_uint4(0, 0, 0, 0)
+                      : SPLIT ? *reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + e)
+                              : *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + e);
+    }
   };
   // turns the loaded queries into operands
   auto take_queries = [&]() {
     if (!live) return;
-    float x[U][16];
+    float x[16 * U];
     uint32_t top = 0;
     #pragma unroll
-    for (int c = 0; c < U; ++c) {
+    for (int i = 0; i < NRAW; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
       #pragma unroll
-      for (int i = 0; i < (SPLIT ? 4 : 2); ++i) {
-        const uint4 y = raw[(SPLIT ? 4 : 2) * c + i];
-        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-        #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (SPLIT) {
-            x[c][4 * i + e] = __uint_as_float(w[e]);
-          } else {
-            x[c][8 * i + 2 * e] = bf16_lo(w[e]);
-            x[c][8 * i + 2 * e + 1] = bf16_hi(w[e]);
-          }
+      for (int e = 0; e < 4; ++e) {
+        if (SPLIT) {
+          x[4 * i + e] = __uint_as_float(w[e]);
+        } else {
+          x[8 * i + 2 * e] = bf16_lo(w[e]);
+          x[8 * i + 2 * e + 1] = bf16_hi(w[e]);
         }
       }
-      #pragma unroll
-      for (int d = 0; d < 16; ++d) top = max(top, __float_as_uint(x[c][d]) & 0x7fffffffu);
     }
+    #pragma unroll
+    for (int d = 0; d < 16 * U; ++d) top = max(top, __float_as_uint(x[d]) & 0x7fffffffu);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const int e = (int)(top >> 23);                    // q 2^(126 - e) is below 1
@@ -392,21 +402,22 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     qs[0] = __shfl_sync(0xffffffffu, back, 8 * t);
     qs[1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     #pragma unroll
-    for (int c = 0; c < U; ++c)
+    for (int w = 0; w < 4 * U; ++w)
       #pragma unroll
-      for (int w = 0; w < 4; ++w)
-        #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float y0 = x[c][4 * w + 2 * i] * f, y1 = x[c][4 * w + 2 * i + 1] * f;
-          if (SPLIT) split_f16(y0, y1, qh[4 * c + w][i], ql[4 * c + w][i]);
-          else qh[4 * c + w][i] = pack_f16x2(y0, y1);
-        }
+      for (int i = 0; i < 2; ++i) {
+        const float y0 = x[4 * w + 2 * i] * f, y1 = x[4 * w + 2 * i + 1] * f;
+        if (SPLIT) split_f16(y0, y1, qh[w][i], ql[w][i]);
+        else qh[w][i] = pack_f16x2(y0, y1);
+      }
   };
 
+  const float inv_cap = MODS && a.cap > 0.f ? 1.f / a.cap : 0.f;
   auto process = [&](uint8_t* blk, int lp) {
     const float* sc = reinterpret_cast<const float*>(blk + 2 * kPage * HD);
     const float ks = sc[0], lvs = lg2(sc[1]);
-    float ca[4] = {0.f, 0.f, 0.f, 0.f}, cb[4] = {0.f, 0.f, 0.f, 0.f};
+    float ca[4], cb[4];
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) ca[i] = cb[i] = 0.f;
     {
       const uint8_t* kp = blk + (4 * (g >> 1) + (g & 1)) * 64 + t * 16;
       #pragma unroll
@@ -424,53 +435,53 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
         }
       }
     }
-    // this lane's scores: rows 2t + r, tokens 4 (g / 2) + 2j + g % 2
+    // this lane's scores: rows 2t + i, tokens 4 (g / 2) + 2j + g % 2
     const int pos0 = lp * kPage, pos = pos0 + 4 * (g >> 1) + (g & 1);
     const bool whole = pos0 >= tile_lo && pos0 + kPage - 1 <= tile_hi;
-    float c[2][2], y[2][2], thr[2];
+    float c[2][2], y[2][2];
+    bool passed = false;
     #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float f = qs[r] * ks;
+    for (int i = 0; i < 2; ++i) {
+      const float f = qs[i] * ks;
       #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float x = (ca[2 * j + r] + cb[2 * j + r]) * f;
+        float x = (ca[2 * j + i] + cb[2 * j + i]) * f;
         if (MODS) {
-          if (a.cap > 0.f) x = a.cap * tanhf(x / a.cap);
-          // a row that is not there has hi = INT32_MAX and no slope
-          if (a.slopes) x -= slope[r] * (float)(hi[r] - (pos + 2 * j));
+          if (a.cap > 0.f) x = cap_logit<SPLIT>(x, a.cap, inv_cap);
+          if (a.slopes) x -= slope[i] * (float)(at[i] - (pos + 2 * j));   // a row that is not there: 0
           x *= kLog2e;
         }
-        c[r][j] = x;
+        c[i][j] = x;
       }
-      thr[r] = fminf(kSlack, kSlack - lvs - (m[r] - mo[r]));
     }
     if (!whole) {
       #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int i = 0; i < 2; ++i)
         #pragma unroll
         for (int j = 0; j < 2; ++j)
-          if (pos + 2 * j < lo[r] || pos + 2 * j > hi[r]) c[r][j] = -INFINITY;
+          if (pos + 2 * j > at[i] || (a.window > 0 && pos + 2 * j <= at[i] - a.window)) c[i][j] = -INFINITY;
     }
     #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      y[r][0] = c[r][0] - m[r];
-      y[r][1] = c[r][1] - m[r];
+    for (int i = 0; i < 2; ++i) {
+      y[i][0] = c[i][0] - m[i];
+      y[i][1] = c[i][1] - m[i];
+      passed |= fmaxf(y[i][0], y[i][1]) > fminf(kSlack, kSlack - lvs - (m[i] - mo[i]));
     }
-    if (__any_sync(0xffffffffu, fmaxf(y[0][0], y[0][1]) > thr[0] || fmaxf(y[1][0], y[1][1]) > thr[1])) {
+    if (__any_sync(0xffffffffu, passed)) {
       float ao[2];
       #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float mx = fmaxf(c[r][0], c[r][1]);
+      for (int i = 0; i < 2; ++i) {
+        float mx = fmaxf(c[i][0], c[i][1]);
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        const float m_new = fmaxf(m[r], mx), mo_new = fmaxf(mo[r], mx + lvs);
-        l[r] *= ex2(m[r] - m_new);
-        ao[r] = ex2(mo[r] - mo_new);
-        m[r] = m_new;
-        mo[r] = mo_new;
-        y[r][0] = c[r][0] - m_new;
-        y[r][1] = c[r][1] - m_new;
+        const float m_new = fmaxf(m[i], mx), mo_new = fmaxf(mo[i], mx + lvs);
+        l[i] *= ex2(m[i] - m_new);
+        ao[i] = ex2(mo[i] - mo_new);
+        m[i] = m_new;
+        mo[i] = mo_new;
+        y[i][0] = c[i][0] - m_new;
+        y[i][1] = c[i][1] - m_new;
       }
       #pragma unroll
       for (int v = 0; v < V4; ++v)
@@ -484,26 +495,28 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     }
     float w[2][2];
     #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int i = 0; i < 2; ++i) {
       // the bound keeps 0 * f a 0; it is passed only where p is below 2^-96
-      const float f = ex2(fminf(lvs + (m[r] - mo[r]) + kLift, 100.f));
+      const float f = ex2(fminf(lvs + (m[i] - mo[i]) + kLift, 100.f));
       #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float p = ex2(y[r][j]);
-        l[r] += p;
-        w[r][j] = p * f;
+        const float p = ex2(y[i][j]);
+        l[i] += p;
+        w[i][j] = p * f;
       }
     }
     if (!whole) {
       // masked tokens weigh nothing, whatever the scales are (a key scale
       // that is not a number was replaced with the score)
       #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int i = 0; i < 2; ++i)
         #pragma unroll
         for (int j = 0; j < 2; ++j)
-          if (c[r][j] == -INFINITY) w[r][j] = 0.f;
-      // value codes of tokens that no row sees may be any bytes: zero them
-      // where this lane reads them (the worker's other warps write the same)
+          if (c[i][j] == -INFINITY) w[i][j] = 0.f;
+      // value codes of tokens that no row of the segment sees may be any
+      // bytes: zero them where this lane reads them (the worker's other warps
+      // write the same)
+      const int any_lo = a.window > 0 ? my_seg->first - a.window + 1 : 0, any_hi = my_seg->last;
       uint32_t keep = 0xffffffffu;
       #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -545,42 +558,44 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     return ll == 0.f ? 0.f : exp2f(mmo - mm - kLift) / ll;
   };
   auto put = [&](int row, int j, int d, float4 y) {       // 4 dims of query row `row`, head j
-    const size_t at = ((size_t)row * H * G + j) * HD + d;
+    const size_t e = ((size_t)row * H * G + j) * HD + d;
     if (SPLIT) {
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = y;
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + e) = y;
     } else {
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + e) =
           make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
     }
   };
   // the warp's rows: to a partial's rows at dst, or (dst null) to the output
   auto flush = [&](float* dst) {
     if (!live) return;
+    const Segment s = *my_seg;
     #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float ll = l[r];
+    for (int i = 0; i < 2; ++i) {
+      float ll = l[i];
       ll += __shfl_xor_sync(0xffffffffu, ll, 4);
       ll += __shfl_xor_sync(0xffffffffu, ll, 8);
       ll += __shfl_xor_sync(0xffffffffu, ll, 16);
       if (gave_up >= 0) ll = __uint_as_float(0x7fc00000u);
-      const int row = wt * ROWS + 2 * t + r;
-      const float f = final_factor(m[r], ll, mo[r]);
-      const int src = r0 + row / G;
-      const bool ok = row < seg_rows && src >= 0 && src < a.n_q;
+      const int row = wt * ROWS + 2 * t + i;
+      const float f = final_factor(m[i], ll, mo[i]);
+      const int src = s.r0 + row / G;
+      const bool ok = row < s.rows && src >= 0 && src < a.n_q;
       #pragma unroll
       for (int v = 0; v < V4; ++v) {
-        const float4 y = make_float4(o[v][0][r], o[v][0][2 + r], o[v][1][r], o[v][1][2 + r]);
+        const float4 y = make_float4(o[v][0][i], o[v][0][2 + i], o[v][1][i], o[v][1][2 + i]);
         const int d = 4 * (8 * v + g);
         if (dst) *reinterpret_cast<float4*>(dst + (size_t)row * SROW + d) = y;
-        else if (ok) put(src, h * G + row % G, d, make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
+        else if (ok) put(src, s.h * G + row % G, d, make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
       }
       if (dst && g == 0) {
         float* ml = dst + (size_t)row * SROW + HD;
-        ml[0] = m[r];
+        ml[0] = m[i];
         ml[1] = ll;
-        ml[2] = mo[r];
+        ml[2] = mo[i];
       }
     }
+    __syncwarp();
   };
   float* my_head = heads + (size_t)worker * NT * ROWS * SROW;
 
@@ -629,9 +644,10 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   const int lag = NT == 1 ? 0 : 1;
   if (n_units > 0) begin_segment(g0);
   {
-    const Page p0 = lookup(lane), p1 = n_units > 32 ? lookup(32 + lane) : Page{-1, -1, 0, 0};
-    found(p0, bl0, lg0);
-    found(p1, bl1, lg1);
+    lookup(lane, bl0, lg0);
+    if (n_units > 32) lookup(32 + lane, bl1, lg1);
+    found(lane, bl0, lg0);
+    if (n_units > 32) found(32 + lane, bl1, lg1);
   }
   if (wt == 0) {
     #pragma unroll 1
@@ -639,13 +655,13 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   }
   take_queries();
   find_cuts();
-  Page coming = {-1, -1, 0, 0};
   #pragma unroll 1
   for (int k = 0;; ++k) {
     if (k == n_units || g0 + k == seg_end) {
       if (k > 0) {
-        float* dst = seg_begin < g0 ? my_head : nullptr;
-        if (k == n_units && seg_begin >= g0 && seg_end > g1) {
+        const bool head = my_seg->begin < g0;
+        float* dst = head ? my_head : nullptr;
+        if (k == n_units && !head && seg_end > g1) {
           // the tail goes into the worker's own ring, which is idle now
           if (NT > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + worker), "r"(32 * NT) : "memory");
           dst = reinterpret_cast<float*>(my_ring);
@@ -660,9 +676,9 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
       base = k;
       bl0 = bl1;
       lg0 = lg1;
-      coming = lookup(k + 32 + lane);
+      lookup(k + 32 + lane, bl1, lg1);
     }
-    if ((k & 31) == 16 && k > 16) found(coming, bl1, lg1);      // the ring is at most 16 pages ahead
+    if ((k & 31) == 16 && k > 16) found(k + 16 + lane, bl1, lg1);      // the ring is at most 16 pages ahead
     const int lp = __shfl_sync(0xffffffffu, lg0, k & 31), stage = k & (S - 1);
     if (gave_up < 0) {
       const bool ok = mbar_wait(full0 + 8 * stage, (k >> s_log2) & 1);
@@ -822,8 +838,7 @@ static Attn8Layout attn8_layout(int batch, int H, int rows, int hd) {
 template <int HD, int TYPE, bool SPLIT, bool MODS>
 static cudaError_t attn8_launch(const Attn8Args& g, int grid, cudaStream_t st) {
   auto kern = k_kv8_attn<HD, TYPE, SPLIT, MODS>;
-  const size_t fixed = (size_t)kA8Stages * kv8_block_bytes(HD) + 4ull * kA8Warps * 8 * (HD + 4) +
-                       16ull * kA8Stages;
+  const size_t fixed = (size_t)kA8Stages * kv8_block_bytes(HD) + 4ull * kA8Warps * 8 * (HD + 4) + 16ull * kA8Stages;
   // once per device: the most that any batch needs
   static std::atomic<unsigned long long> ready{0};
   int dev = 0;
