@@ -30,8 +30,8 @@ inline bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_
 
 // Launch with programmatic stream serialisation (the kernel starts with
 // pdl_wait()).
-template <typename K, typename A>
-cudaError_t launch_op(K kern, dim3 grid, dim3 block, size_t smem, cudaStream_t st, const A& a) {
+template <typename K, typename... A>
+cudaError_t launch_op(K kern, dim3 grid, dim3 block, size_t smem, cudaStream_t st, const A&... a) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -42,7 +42,7 @@ cudaError_t launch_op(K kern, dim3 grid, dim3 block, size_t smem, cudaStream_t s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  return cudaLaunchKernelEx(&cfg, kern, a...);
 }
 
 }  // namespace bc

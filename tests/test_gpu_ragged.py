@@ -580,3 +580,24 @@ def test_other_streams():
     s.synchronize()
     top = k.abs().amax().item()
     assert (ko - k).abs().max().item() <= top / 127 / 2 * 1.01 and torch.equal(ko, vo)
+
+
+@pytest.mark.parametrize("hist,bias", [(30000, 0), (30000, 2), (12288, 0), (12286, 2), (12287, 2), (3, 13000)])
+def test_logits_long_lists(hist, bias):
+    """Histories and bias lists on both sides of what a hash table takes, with
+    more distinct ids than it has room for."""
+    V, g = 40000, gen(hist + bias)
+    x = torch.randn(2, V, generator=g)
+    h = torch.cat([torch.randperm(V, generator=g)[:hist], torch.randperm(V, generator=g)[: hist // 2]]).int()
+    hs = np.array([0, hist, hist + hist // 2], np.int32)
+    kw = dict(hist=h.numpy(), hist_start=hs, prompt_len=np.array([hist // 3, 0], np.int32),
+              repetition=np.float32([1.3, 0.8]), frequency=np.float32([0.2, -0.1]), presence=np.float32([0.1, 0.4]))
+    if bias:
+        kw.update(bias_ids=torch.randint(0, V, (2 * bias,), generator=g).int().numpy(),
+                  bias_vals=torch.randn(2 * bias, generator=g).numpy(), bias_start=np.array([0, bias, 2 * bias], np.int32))
+    want = og.logits_adjust(x.double().numpy(), **kw)
+    for out in (torch.full((2, V), 77.0, device=DEV), None):
+        src = x.to(DEV)
+        out = src if out is None else out
+        bc.logits_adjust(src, out, **{k: to(DEV, v) for k, v in kw.items()})
+        assert np.abs(out.cpu().double().numpy() - want).max() <= 5 * 2.0 ** -24 * 20
