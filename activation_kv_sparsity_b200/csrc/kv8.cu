@@ -8,8 +8,14 @@
 // at 64), so m is one warp reduction and nothing is read twice.  Value codes
 // lie four tokens to a word; the lane's 4 tokens x 4 dims are turned by byte
 // permutes, and the lane's words are contiguous (16 bytes a group of tokens).
+// HBM bounds both for prompts, the chain slots - tokens - scale - codes a
+// decode step.  A CTA takes a window of tokens and a group of heads; its
+// warps share the items of the runs that begin there.
 #include "entry.h"
 #include "kv8.cuh"
+
+#include <algorithm>
+#include <type_traits>
 
 namespace bc {
 
@@ -19,7 +25,7 @@ struct Kv8AppendArgs {
   const int* slots;
   int n_tokens, n_pages, H;
   uint8_t* pool;
-  int window;     // tokens whose runs one warp handles
+  int window, heads;     // tokens and kv heads per CTA
 };
 
 struct Kv8GatherArgs {
@@ -28,17 +34,18 @@ struct Kv8GatherArgs {
   const int* slots;
   int n_tokens;
   void *k, *v;
-  int window;
+  int window, heads;
 };
 
-constexpr int kKv8Threads = 128;
+constexpr int kKv8Warps = 8, kKv8Threads = kKv8Warps * 32, kKv8Ctas = 3;   // CTAs per SM
 
-// The runs that begin in tokens [t0, t0 + window), window <= 16: calls
-// body(first token, slot of it, tokens) for each, warp-uniform.  A run ends
-// with its page.
+// The runs that begin in tokens [t0, t0 + window), window <= 16, and for each
+// the 2 * heads items of keys and values: calls body(first token, slot of it,
+// tokens, item) for this warp's share.  A run ends with its page.
 template <typename F>
-__device__ __forceinline__ void for_each_run(const int* slots, int n, int t0, int window, int n_slots, F body) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void for_each_item(const int* slots, int n, int t0, int window, int n_slots, int items,
+                                              F body) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = t0 - 1 + lane;                      // lane 0: the token before the window
   int s = i >= 0 && i < n ? slots[i] : -1;
   if (s >= n_slots) s = -1;
@@ -46,170 +53,206 @@ __device__ __forceinline__ void for_each_run(const int* slots, int n, int t0, in
   const bool joins = lane > 0 && s >= 0 && prev >= 0 && s == prev + 1 && s % kPage != 0;
   const unsigned jm = __ballot_sync(0xffffffffu, joins);
   unsigned heads = __ballot_sync(0xffffffffu, s >= 0 && !joins && lane >= 1 && lane <= window);
+  int item = warp;                                  // of all runs' items, one after the other
   while (heads) {
     const int l = __ffs(heads) - 1;
     heads &= heads - 1;
     // lanes l + 1, l + 2, ... that join: at most 15, since a run ends with its page
     const unsigned follow = l < 31 ? ~(jm >> (l + 1)) : 1u;
-    const int cnt = 1 + min(__ffs(follow) - 1, 31 - l);
-    body(t0 - 1 + l, __shfl_sync(0xffffffffu, s, l), cnt);
+    const int cnt = 1 + min(__ffs(follow) - 1, 31 - l), slot = __shfl_sync(0xffffffffu, s, l);
+    for (; item < items; item += kKv8Warps) body(t0 - 1 + l, slot, cnt, item);
+    item -= items;
   }
 }
 
+// Four neighbouring elements as loaded: their values, and the largest |x| as
+// an ordered integer (infinities and NaN come out on top).
 template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
+struct Raw;
 template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
+struct Raw<float> {
+  uint4 w;
+  __device__ __forceinline__ void load(const float* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ float4 get() const {
+    return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+  }
+  __device__ __forceinline__ void top(uint32_t& t) const {
+    t = max(t, max(max(w.x & 0x7fffffffu, w.y & 0x7fffffffu), max(w.z & 0x7fffffffu, w.w & 0x7fffffffu)));
+  }
+  static __device__ __forceinline__ uint32_t bits(uint32_t t) { return t; }
+};
 template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-}
+struct Raw<__nv_bfloat16> {
+  uint2 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void zero() { w = make_uint2(0, 0); }
+  __device__ __forceinline__ float4 get() const { return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)); }
+  // two 16-bit maxima side by side
+  __device__ __forceinline__ void top(uint32_t& t) const {
+    t = __vmaxu2(t, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu));
+  }
+  static __device__ __forceinline__ uint32_t bits(uint32_t t) { return max(t & 0xffffu, t >> 16) << 16; }
+};
 __device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
 }
 
 template <int HD, int TYPE, typename T>
-__global__ void __launch_bounds__(kKv8Threads) k_kv8_append(Kv8AppendArgs a) {
+__global__ void __launch_bounds__(kKv8Threads, kKv8Ctas) k_kv8_append(Kv8AppendArgs a) {
   using C = Kv8Code<TYPE>;
   constexpr int LPT = HD / 4;          // lanes per token
   constexpr int NTOK = kPage * LPT / 32;   // tokens per lane
   const int lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * (kKv8Threads / 32) + (threadIdx.x >> 5);
-  const int part = (int)(item & 1), h = (int)((item >> 1) % a.H);
-  const long long t0 = (item >> 1) / a.H * a.window;
+  const int t0 = blockIdx.x * a.window, head0 = blockIdx.y * a.heads;
   pdl_wait();
   pdl_trigger();
-  if (t0 >= a.n_tokens) return;
   const int d = (lane % LPT) * 4, p0 = (lane / LPT) * NTOK;
-  const T* src = static_cast<const T*>(part ? a.v : a.k) + (long long)h * HD + d;
-  const long long stride = part ? a.v_stride : a.k_stride;
 
-  for_each_run(a.slots, a.n_tokens, (int)t0, a.window, a.n_pages * kPage, [&](int t, int slot, int cnt) {
-    const int off = slot % kPage, end = off + cnt;
+  for_each_item(a.slots, a.n_tokens, t0, a.window, a.n_pages * kPage, 2 * min(a.heads, a.H - head0),
+                [&](int t, int slot, int cnt, int item) {
+    const int part = item & 1, h = head0 + (item >> 1), off = slot % kPage, end = off + cnt;
+    const long long stride = part ? a.v_stride : a.k_stride;
+    // the lane's first token, if it were one of the run
+    const T* src = static_cast<const T*>(part ? a.v : a.k) + (long long)h * HD + d + (t + p0 - off) * stride;
     uint8_t* blk = a.pool + ((long long)(slot / kPage) * a.H + h) * kv8_block_bytes(HD);
     float* scale = reinterpret_cast<float*>(blk + 2 * kPage * HD) + part;
-    const float s_old = off > 0 ? *scale : 0.f;
-    float4 x[NTOK];
-    uint32_t top = 0;                  // |x| as an ordered integer: infinities and NaN come out on top
-    #pragma unroll
-    for (int i = 0; i < NTOK; ++i) {
-      const int p = p0 + i;
-      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p >= off && p < end) x[i] = load4<T>(src + (long long)(t + p - off) * stride);
-      const uint32_t m = max(max(__float_as_uint(x[i].x) & 0x7fffffffu, __float_as_uint(x[i].y) & 0x7fffffffu),
-                             max(__float_as_uint(x[i].z) & 0x7fffffffu, __float_as_uint(x[i].w) & 0x7fffffffu));
-      top = max(top, m);
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
-    float s;
-    if (top >= 0x7f800000u || s_old != s_old) {
-      s = __uint_as_float(0x7fc00000u);
-    } else {
-      s = top ? fmaxf(__fdiv_rn(__uint_as_float(top), C::kMax), 1.17549435e-38f) : 0.f;
-      s = fmaxf(s_old, s);
-    }
-    const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-    const bool grown = off > 0 && s > s_old;
-    uint32_t code[NTOK];
-    #pragma unroll
-    for (int i = 0; i < NTOK; ++i)
-      code[i] = C::encode(x[i].x * inv, x[i].y * inv, x[i].z * inv, x[i].w * inv);
-    auto again = [&](uint32_t w) {     // an earlier token's codes under the new scale
-      const float4 y = kv8_decode4<TYPE>(w);
-      return C::encode(y.x * s_old * inv, y.y * s_old * inv, y.z * s_old * inv, y.w * s_old * inv);
-    };
-    if (part == 0) {
+    // a whole page (most of a prompt) needs no questions about its tokens
+    auto write = [&](auto whole_page) {
+      constexpr bool WHOLE = decltype(whole_page)::value;
+      const float s_old = !WHOLE && off > 0 ? *scale : 0.f;
+      Raw<T> raw[NTOK];
+      uint32_t top = 0;
       #pragma unroll
       for (int i = 0; i < NTOK; ++i) {
-        const int p = p0 + i;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(blk + kv8_k_at(p, d));
-        if (p < off) {
-          if (grown) *dst = again(*dst);
-        } else if (p < end || off == 0) {
-          *dst = code[i];              // zeros behind the run of a fresh page
-        }
+        raw[i].zero();
+        if (WHOLE || (p0 + i >= off && p0 + i < end)) raw[i].load(src + i * stride);
       }
-    } else {
-      uint8_t* vb = blk + kPage * HD + d * kPage;
       #pragma unroll
-      for (int g = 0; g < NTOK / 4; ++g) {
-        const int p = p0 + 4 * g;
-        uint4* dst = reinterpret_cast<uint4*>(vb + p * 4);
-        const bool any = off == 0 || (p < end && (grown || p + 4 > off));
-        if (!any) continue;
-        uint32_t w[4] = {code[4 * g], code[4 * g + 1], code[4 * g + 2], code[4 * g + 3]};
-        if (off > 0) {
-          uint4 o4 = *dst;
-          transpose4x4(o4.x, o4.y, o4.z, o4.w);
-          const uint32_t old[4] = {o4.x, o4.y, o4.z, o4.w};
-          #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (p + j < off) w[j] = grown ? again(old[j]) : old[j];
-            else if (p + j >= end) w[j] = old[j];
+      for (int i = 0; i < NTOK; ++i) raw[i].top(top);
+      top = __reduce_max_sync(0xffffffffu, Raw<T>::bits(top));
+      float s;
+      if (top >= 0x7f800000u || s_old != s_old) {
+        s = __uint_as_float(0x7fc00000u);
+      } else {
+        s = top ? fmaxf(__fdiv_rn(__uint_as_float(top), C::kMax), 1.17549435e-38f) : 0.f;
+        s = fmaxf(s_old, s);
+      }
+      const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+      const bool grown = !WHOLE && off > 0 && s > s_old;
+      uint32_t code[NTOK];
+      #pragma unroll
+      for (int i = 0; i < NTOK; ++i) {
+        const float4 x = raw[i].get();
+        code[i] = C::encode(__fmul_rn(x.x, inv), __fmul_rn(x.y, inv), __fmul_rn(x.z, inv), __fmul_rn(x.w, inv));
+      }
+      auto again = [&](uint32_t w) {     // an earlier token's codes under the new scale
+        const float4 y = kv8_decode4<TYPE>(w);
+        auto f = [&](float v) { return __fmul_rn(__fmul_rn(v, s_old), inv); };
+        return C::encode(f(y.x), f(y.y), f(y.z), f(y.w));
+      };
+      if (part == 0) {
+        uint8_t* kb = blk + kv8_k_at(p0, d);
+        #pragma unroll
+        for (int i = 0; i < NTOK; ++i) {
+          uint32_t* dst = reinterpret_cast<uint32_t*>(kb + 64 * i);
+          if (!WHOLE && p0 + i < off) {
+            if (grown) *dst = again(*dst);
+          } else if (WHOLE || p0 + i < end || off == 0) {
+            *dst = code[i];              // zeros behind the run of a fresh page
           }
         }
-        transpose4x4(w[0], w[1], w[2], w[3]);
-        *dst = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        uint8_t* vb = blk + kPage * HD + d * kPage + p0 * 4;
+        #pragma unroll
+        for (int g = 0; g < NTOK / 4; ++g) {
+          const int p = p0 + 4 * g;
+          uint4* dst = reinterpret_cast<uint4*>(vb + 16 * g);
+          if (!WHOLE && off > 0 && (p >= end || (!grown && p + 4 <= off))) continue;
+          uint32_t w[4] = {code[4 * g], code[4 * g + 1], code[4 * g + 2], code[4 * g + 3]};
+          if (!WHOLE && off > 0) {
+            uint4 o4 = *dst;
+            transpose4x4(o4.x, o4.y, o4.z, o4.w);
+            const uint32_t old[4] = {o4.x, o4.y, o4.z, o4.w};
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (p + j < off) w[j] = grown ? again(old[j]) : old[j];
+              else if (p + j >= end) w[j] = old[j];
+            }
+          }
+          transpose4x4(w[0], w[1], w[2], w[3]);
+          *dst = make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
-    }
-    __syncwarp();
-    if (lane == 0) *scale = s;
+      __syncwarp();
+      if (lane == 0) *scale = s;
+    };
+    if (cnt == kPage) write(std::true_type{});
+    else write(std::false_type{});
   });
 }
 
 template <int HD, int TYPE, typename T>
-__global__ void __launch_bounds__(kKv8Threads) k_kv8_gather(Kv8GatherArgs a) {
+__global__ void __launch_bounds__(kKv8Threads, kKv8Ctas) k_kv8_gather(Kv8GatherArgs a) {
   constexpr int LPT = HD / 4;
   constexpr int NTOK = kPage * LPT / 32;
   const int lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * (kKv8Threads / 32) + (threadIdx.x >> 5);
-  const int part = (int)(item & 1), h = (int)((item >> 1) % a.H);
-  const long long t0 = (item >> 1) / a.H * a.window;
+  const int t0 = blockIdx.x * a.window, head0 = blockIdx.y * a.heads, heads = min(a.heads, a.H - head0);
   pdl_wait();
   pdl_trigger();
-  if (t0 >= a.n_tokens) return;
   const int d = (lane % LPT) * 4, p0 = (lane / LPT) * NTOK;
-  T* out = static_cast<T*>(part ? a.v : a.k) + (long long)h * HD + d;
   const long long row = (long long)a.H * HD;
   // slots outside the pool give zeros
-  for (int i = lane / LPT; i < a.window && t0 + i < a.n_tokens; i += 32 / LPT) {
+  for (int i = threadIdx.x >> 5; i < a.window && t0 + i < a.n_tokens; i += kKv8Warps) {
     const int s = a.slots[t0 + i];
-    if (s < 0 || s >= a.n_pages * kPage) store4(out + (t0 + i) * row, make_float4(0.f, 0.f, 0.f, 0.f));
+    if (s >= 0 && s < a.n_pages * kPage) continue;
+    for (int e = 4 * lane; e < heads * HD; e += 128) {
+      store4(static_cast<T*>(a.k) + (t0 + i) * row + head0 * HD + e, make_float4(0.f, 0.f, 0.f, 0.f));
+      store4(static_cast<T*>(a.v) + (t0 + i) * row + head0 * HD + e, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
   }
-  for_each_run(a.slots, a.n_tokens, (int)t0, a.window, a.n_pages * kPage, [&](int t, int slot, int cnt) {
-    const int off = slot % kPage, end = off + cnt;
+  for_each_item(a.slots, a.n_tokens, t0, a.window, a.n_pages * kPage, 2 * heads,
+                [&](int t, int slot, int cnt, int item) {
+    const int part = item & 1, h = head0 + (item >> 1), off = slot % kPage, end = off + cnt;
     const uint8_t* blk = a.pool + ((long long)(slot / kPage) * a.H + h) * kv8_block_bytes(HD);
-    const float s = reinterpret_cast<const float*>(blk + 2 * kPage * HD)[part];
-    uint32_t w[NTOK];
-    if (part == 0) {
+    // the lane's first token, if it were one of the run
+    T* out = static_cast<T*>(part ? a.v : a.k) + (long long)h * HD + d + (t + p0 - off) * row;
+    auto read = [&](auto whole_page) {
+      constexpr bool WHOLE = decltype(whole_page)::value;
+      const float s = reinterpret_cast<const float*>(blk + 2 * kPage * HD)[part];
+      uint32_t w[NTOK];
+      if (part == 0) {
+        const uint8_t* kb = blk + kv8_k_at(p0, d);
+        #pragma unroll
+        for (int i = 0; i < NTOK; ++i)
+          w[i] = WHOLE || (p0 + i >= off && p0 + i < end) ? *reinterpret_cast<const uint32_t*>(kb + 64 * i) : 0u;
+      } else {
+        const uint8_t* vb = blk + kPage * HD + d * kPage + p0 * 4;
+        uint4 x[NTOK / 4];
+        #pragma unroll
+        for (int g = 0; g < NTOK / 4; ++g) {
+          x[g] = make_uint4(0, 0, 0, 0);
+          if (WHOLE || (p0 + 4 * g < end && p0 + 4 * g + 4 > off)) x[g] = *reinterpret_cast<const uint4*>(vb + 16 * g);
+        }
+        #pragma unroll
+        for (int g = 0; g < NTOK / 4; ++g) {
+          transpose4x4(x[g].x, x[g].y, x[g].z, x[g].w);
+          w[4 * g] = x[g].x;
+          w[4 * g + 1] = x[g].y;
+          w[4 * g + 2] = x[g].z;
+          w[4 * g + 3] = x[g].w;
+        }
+      }
       #pragma unroll
       for (int i = 0; i < NTOK; ++i) {
-        const int p = p0 + i;
-        w[i] = p >= off && p < end ? *reinterpret_cast<const uint32_t*>(blk + kv8_k_at(p, d)) : 0u;
-      }
-    } else {
-      #pragma unroll
-      for (int g = 0; g < NTOK / 4; ++g) {
-        const int p = p0 + 4 * g;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (p < end && p + 4 > off) x = *reinterpret_cast<const uint4*>(blk + kPage * HD + d * kPage + p * 4);
-        transpose4x4(x.x, x.y, x.z, x.w);
-        w[4 * g] = x.x;
-        w[4 * g + 1] = x.y;
-        w[4 * g + 2] = x.z;
-        w[4 * g + 3] = x.w;
-      }
-    }
-    #pragma unroll
-    for (int i = 0; i < NTOK; ++i) {
-      const int p = p0 + i;
-      if (p >= off && p < end) {
+        if (!WHOLE && (p0 + i < off || p0 + i >= end)) continue;
         const float4 y = kv8_decode4<TYPE>(w[i]);
-        store4(out + (long long)(t + p - off) * row, make_float4(y.x * s, y.y * s, y.z * s, y.w * s));
+        store4(out + i * row, make_float4(y.x * s, y.y * s, y.z * s, y.w * s));
       }
-    }
+    };
+    if (cnt == kPage) read(std::true_type{});
+    else read(std::false_type{});
   });
 }
 
@@ -229,20 +272,22 @@ static bc_status kv8_check(const char* who, const void* pool, int type, int n_pa
   if (!kv8_sizes_ok(n_pages, H, hd)) return entry_fail(BC_EINVAL, "%s: bad n_pages or n_kv_heads", who);
   if (type != BC_KV8_E4M3 && type != BC_KV8_INT8) return entry_fail(BC_EINVAL, "%s: bad code type %d", who, type);
   if (dtype != BC_F32 && dtype != BC_BF16) return entry_fail(BC_EINVAL, "%s: bad dtype %d", who, dtype);
-  if (n_tokens < 0) return entry_fail(BC_EINVAL, "%s: n_tokens < 0", who);
+  if (n_tokens < 0 || n_tokens > INT32_MAX - 64) return entry_fail(BC_EINVAL, "%s: bad n_tokens %d", who, n_tokens);
   return BC_OK;
 }
 
-// One token a warp while that leaves the GPU room, else a page's worth of
-// tokens (whose runs, one or two for a prompt, the warp takes in turn).
-static int kv8_window(int n_tokens) { return n_tokens <= 2048 ? 1 : kPage; }
-
-static bc_status kv8_grid(const char* who, int n_tokens, int window, int H, unsigned* grid) {
-  const long long warps = (n_tokens + (long long)window - 1) / window * H * 2;
-  const long long g = (warps + kKv8Threads / 32 - 1) / (kKv8Threads / 32);
-  if (g > INT32_MAX) return entry_fail(BC_EINVAL, "%s: too many tokens and heads for one call", who);
-  *grid = (unsigned)g;
-  return BC_OK;
+// Windows of a page's worth of tokens (one or two runs of a prompt) and 8
+// heads, of fewer heads and then of 4 tokens (a decode step has a run a token)
+// until there is a CTA for every place on the GPU.
+static dim3 kv8_grid(int n_tokens, int H, int* window, int* heads) {
+  constexpr long long kPlaces = 148 * kKv8Ctas;
+  *window = kPage;
+  *heads = std::min(H, 8);
+  auto windows = [&]() { return (n_tokens + (long long)*window - 1) / *window; };
+  auto groups = [&]() { return (H + *heads - 1) / *heads; };
+  while (*heads > 1 && windows() * groups() < kPlaces) *heads = (*heads + 1) / 2;
+  while (*window > 4 && windows() * groups() < kPlaces) *window /= 2;
+  return dim3((unsigned)windows(), (unsigned)groups());
 }
 
 #define KV8_LAUNCH(KERN, ...)                                                                                \
@@ -282,13 +327,10 @@ extern "C" bc_status bc_kv8_append(const void* k, const void* v, bc_dtype dtype,
   const long long least = (long long)n_kv_heads * head_dim;
   if (k_stride < least || v_stride < least || k_stride % 4 || v_stride % 4)
     return entry_fail(BC_EINVAL, "%s: strides must be multiples of 4 and at least n_kv_heads * head_dim", who);
-  Kv8AppendArgs a{k, v, k_stride, v_stride, slots, n_tokens, n_pages, n_kv_heads, static_cast<uint8_t*>(pool),
-                  kv8_window(n_tokens)};
-  unsigned grid;
-  s = kv8_grid(who, n_tokens, a.window, n_kv_heads, &grid);
-  if (s != BC_OK) return s;
+  Kv8AppendArgs a{k, v, k_stride, v_stride, slots, n_tokens, n_pages, n_kv_heads, static_cast<uint8_t*>(pool), 0, 0};
+  const dim3 grid = kv8_grid(n_tokens, n_kv_heads, &a.window, &a.heads);
   cudaError_t e;
-  KV8_LAUNCH(k_kv8_append, dim3(grid), dim3(kKv8Threads), 0, static_cast<cudaStream_t>(stream), a);
+  KV8_LAUNCH(k_kv8_append, grid, dim3(kKv8Threads), 0, static_cast<cudaStream_t>(stream), a);
   return entry_cuda(e, who);
 }
 
@@ -302,12 +344,9 @@ extern "C" bc_status bc_kv8_gather(const void* pool, bc_kv8_type type, int n_pag
   if (!k_out || !v_out || !slots) return entry_fail(BC_EINVAL, "%s: null pointer", who);
   if (!aligned(k_out, 16) || !aligned(v_out, 16))
     return entry_fail(BC_EINVAL, "%s: outputs must be 16-byte aligned", who);
-  Kv8GatherArgs a{static_cast<const uint8_t*>(pool), n_pages, n_kv_heads, slots, n_tokens, k_out, v_out,
-                  kv8_window(n_tokens)};
-  unsigned grid;
-  s = kv8_grid(who, n_tokens, a.window, n_kv_heads, &grid);
-  if (s != BC_OK) return s;
+  Kv8GatherArgs a{static_cast<const uint8_t*>(pool), n_pages, n_kv_heads, slots, n_tokens, k_out, v_out, 0, 0};
+  const dim3 grid = kv8_grid(n_tokens, n_kv_heads, &a.window, &a.heads);
   cudaError_t e;
-  KV8_LAUNCH(k_kv8_gather, dim3(grid), dim3(kKv8Threads), 0, static_cast<cudaStream_t>(stream), a);
+  KV8_LAUNCH(k_kv8_gather, grid, dim3(kKv8Threads), 0, static_cast<cudaStream_t>(stream), a);
   return entry_cuda(e, who);
 }

@@ -39,10 +39,11 @@ struct Kv8Code<0> {
 template <>
 struct Kv8Code<1> {
   static constexpr float kMax = 127.f;
-  static __device__ __forceinline__ int round1(float x) { return max(-127, min(127, __float2int_rn(x))); }
+  // 1.5 2^23 + x has the rounded x (ties to even) in its low bits; a value
+  // divided by its scale is at most 127 (1 + 2^-23), so nothing to clamp
   static __device__ __forceinline__ uint32_t encode(float x0, float x1, float x2, float x3) {
-    const uint32_t lo = __byte_perm((uint32_t)round1(x0), (uint32_t)round1(x1), 0x0040);
-    const uint32_t hi = __byte_perm((uint32_t)round1(x2), (uint32_t)round1(x3), 0x0040);
+    const uint32_t lo = __byte_perm(__float_as_uint(x0 + 12582912.f), __float_as_uint(x1 + 12582912.f), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(x2 + 12582912.f), __float_as_uint(x3 + 12582912.f), 0x0040);
     return __byte_perm(lo, hi, 0x5410);
   }
   // a code c is the f16 number 0x6400 | (c + 128) = 1024 + (c + 128), less
