@@ -20,8 +20,19 @@ _DTYPES = {torch.float32: BC_F32, torch.bfloat16: BC_BF16}
 _BLOCKS = {32 * hd + 32: hd for hd in (64, 128)}       # block bytes -> head_dim
 
 
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
+
+
+# A call's checks are one expression over _is(); only when it fails do the
+# checks below go through the arguments one by one to say which is wrong.
+def _is(t, dtype, dev, n):
+    """A contiguous tensor of dtype with n entries on device number dev."""
+    return t.dtype is dtype and t.get_device() == dev and t.numel() == n and t.is_contiguous()
+
+
 def _dense(who, dev, dtype, **tensors):
-    """Checks contiguous tensors of a type on device number dev; None passes."""
+    """Raises for a tensor that is not contiguous, of dtype and on device
+    number dev; None passes."""
     for name, t in tensors.items():
         if t is not None and (t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()):
             raise ValueError(f"{who}: {name} must be a contiguous {dtype} tensor on cuda:{dev}")
@@ -80,28 +91,30 @@ def block_tables(lens, delta, table, free_list, n_free, lens_out, n_free_out, q_
     if not table.is_cuda or table.dim() != 2:
         raise ValueError(f"{who}: table must be a CUDA tensor [batch][max_blocks]")
     dev = table.get_device()
-    _dense(who, dev, torch.int32, lens=lens, delta=delta, table=table, free_list=free_list, n_free=n_free,
-           lens_out=lens_out, n_free_out=n_free_out, q_start=q_start, slots=slots, positions=positions, ticket=ticket)
     B, max_blocks = table.shape
-    n = slots.numel()
-    _sizes(who, lens=(lens, B), delta=(delta, B), lens_out=(lens_out, B), q_start=(q_start, B + 1),
-           n_free=(n_free, 1), n_free_out=(n_free_out, 1), ticket=(ticket, 1), positions=(positions, n))
-    a = bc_block_tables_args(B, max_blocks, free_list.numel(), n, lens.data_ptr(), delta.data_ptr(),
+    n, n_pages = slots.numel(), free_list.numel()
+    if not (_is(lens, _I32, dev, B) and _is(delta, _I32, dev, B) and _is(table, _I32, dev, B * max_blocks)
+            and _is(free_list, _I32, dev, n_pages) and _is(n_free, _I32, dev, 1) and _is(lens_out, _I32, dev, B)
+            and _is(n_free_out, _I32, dev, 1) and _is(q_start, _I32, dev, B + 1) and _is(slots, _I32, dev, n)
+            and _is(positions, _I32, dev, n) and _is(ticket, _I32, dev, 1)):
+        _dense(who, dev, _I32, lens=lens, delta=delta, table=table, free_list=free_list, n_free=n_free,
+               lens_out=lens_out, n_free_out=n_free_out, q_start=q_start, slots=slots, positions=positions,
+               ticket=ticket)
+        _sizes(who, lens=(lens, B), delta=(delta, B), lens_out=(lens_out, B), q_start=(q_start, B + 1),
+               n_free=(n_free, 1), n_free_out=(n_free_out, 1), ticket=(ticket, 1), positions=(positions, n))
+    a = bc_block_tables_args(B, max_blocks, n_pages, n, lens.data_ptr(), delta.data_ptr(),
                              table.data_ptr(), free_list.data_ptr(), n_free.data_ptr(), lens_out.data_ptr(),
                              n_free_out.data_ptr(), q_start.data_ptr(), slots.data_ptr(), positions.data_ptr(),
                              ticket.data_ptr())
     _call(dev, stream, "bc_block_tables", bc_block_tables, C.byref(a))
 
 
-def _rows(who, dev, shape, **tensors):
-    """Checks [n][H][hd] tensors of one type whose heads and dims are dense."""
-    first = None
-    for name, t in tensors.items():
-        first = t if first is None else first
-        if t.shape != shape or t.dtype is not first.dtype or t.get_device() != dev:
-            raise ValueError(f"{who}: {name} must be {list(shape)} on cuda:{dev}, all of one type")
-        if t.numel() and (t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2])):
-            raise ValueError(f"{who}: heads and dims of {name} must be dense")
+def _rows(who, dev, shape, t, name, dtype):
+    """Checks an [n][H][hd] tensor whose heads and dims are dense."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{who}: {name} must be {dtype} {list(shape)} on cuda:{dev}")
+    if not t.is_contiguous() and t.numel() and (t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2])):
+        raise ValueError(f"{who}: heads and dims of {name} must be dense")
 
 
 def kv8_append(k, v, slots, pool, code="e4m3", stream=None):
@@ -111,9 +124,11 @@ def kv8_append(k, v, slots, pool, code="e4m3", stream=None):
     who = "kv8_append"
     P, H, hd, dev = _pool(who, pool)
     n = slots.numel()
-    _dense(who, dev, torch.int32, slots=slots)
-    _rows(who, dev, (n, H, hd), k=k, v=v)
+    if not _is(slots, _I32, dev, n):
+        _dense(who, dev, _I32, slots=slots)
     dt, typ = _dtype(who, k), _code(who, code)
+    _rows(who, dev, (n, H, hd), k, "k", k.dtype)
+    _rows(who, dev, (n, H, hd), v, "v", k.dtype)
     if n == 0:
         return
     ks, vs = (k.stride(0), v.stride(0)) if n > 1 else (H * hd, H * hd)
@@ -127,10 +142,13 @@ def kv8_gather(pool, slots, k_out, v_out, code="e4m3", stream=None):
     who = "kv8_gather"
     P, H, hd, dev = _pool(who, pool)
     n = slots.numel()
-    _dense(who, dev, torch.int32, slots=slots)
-    _rows(who, dev, (n, H, hd), k_out=k_out, v_out=v_out)
-    _dense(who, dev, k_out.dtype, k_out=k_out, v_out=v_out)
+    if not _is(slots, _I32, dev, n):
+        _dense(who, dev, _I32, slots=slots)
     dt, typ = _dtype(who, k_out), _code(who, code)
+    _rows(who, dev, (n, H, hd), k_out, "k_out", k_out.dtype)
+    _rows(who, dev, (n, H, hd), v_out, "v_out", k_out.dtype)
+    if not (k_out.is_contiguous() and v_out.is_contiguous()):
+        raise ValueError(f"{who}: k_out and v_out must be contiguous")
     if n == 0:
         return
     _call(dev, stream, "bc_kv8_gather", bc_kv8_gather, pool.data_ptr(), typ, P, H, hd, slots.data_ptr(), n,
@@ -151,16 +169,22 @@ def kv8_attention(q, pool, lens, table, out, scratch, code="e4m3", q_start=None,
     if q.dim() != 3 or q.shape[1] % H or q.shape[1] == 0:
         raise ValueError(f"{who}: q must be [n_q][a multiple of {H}][{hd}]")
     n_q, Hq, _ = q.shape
-    _rows(who, dev, (n_q, Hq, hd), q=q, out=out)
     dt, typ = _dtype(who, q), _code(who, code)
+    _rows(who, dev, (n_q, Hq, hd), q, "q", q.dtype)
+    _rows(who, dev, (n_q, Hq, hd), out, "out", q.dtype)
     if table.dim() != 2:
         raise ValueError(f"{who}: table must be [batch][max_blocks]")
     B, max_blocks = table.shape
-    _dense(who, dev, q.dtype, out=out)
-    _dense(who, dev, torch.int32, lens=lens, table=table, q_start=q_start, pages=pages, n_sel=n_sel)
-    _dense(who, dev, torch.uint8, scratch=scratch)
-    _dense(who, dev, torch.float32, slopes=slopes)
-    _sizes(who, lens=(lens, B), q_start=(q_start, B + 1), n_sel=(n_sel, B), slopes=(slopes, Hq))
+    if not (out.is_contiguous() and _is(lens, _I32, dev, B) and _is(table, _I32, dev, B * max_blocks)
+            and scratch.dtype is _U8 and scratch.get_device() == dev and scratch.is_contiguous()
+            and (q_start is None or _is(q_start, _I32, dev, B + 1)) and (n_sel is None or _is(n_sel, _I32, dev, B))
+            and (pages is None or (pages.dtype is _I32 and pages.get_device() == dev and pages.is_contiguous()))
+            and (slopes is None or _is(slopes, _F32, dev, Hq))):
+        _dense(who, dev, q.dtype, out=out)
+        _dense(who, dev, _I32, lens=lens, table=table, q_start=q_start, pages=pages, n_sel=n_sel)
+        _dense(who, dev, _U8, scratch=scratch)
+        _dense(who, dev, _F32, slopes=slopes)
+        _sizes(who, lens=(lens, B), q_start=(q_start, B + 1), n_sel=(n_sel, B), slopes=(slopes, Hq))
     if q_start is None and (max_q != 1 or n_q != B):
         raise ValueError(f"{who}: without q_start there is one query row per sequence")
     max_sel = 0
@@ -203,21 +227,28 @@ def logits_adjust(logits, out, hist=None, hist_start=None, prompt_len=None, repe
         raise ValueError(f"{who}: bias_ids, bias_vals and bias_start go together")
     if mask is None and mask_row is not None:
         raise ValueError(f"{who}: mask_row needs mask")
-    _dense(who, dev, torch.int32, hist=hist, hist_start=hist_start, prompt_len=prompt_len, bias_ids=bias_ids,
-           bias_start=bias_start, mask=mask, mask_row=mask_row)
-    _dense(who, dev, torch.float32, repetition=repetition, frequency=frequency, presence=presence, bias_vals=bias_vals)
-    n_hist = n_bias = n_masks = 0
-    if hist is not None:
-        n_hist = hist.numel()
-    if bias_ids is not None:
-        n_bias = bias_ids.numel()
+    n_hist = 0 if hist is None else hist.numel()
+    n_bias = 0 if bias_ids is None else bias_ids.numel()
+    n_masks = 0
     if mask is not None:
         if mask.dim() != 2 or mask.shape[1] != (V + 31) // 32:
             raise ValueError(f"{who}: mask must be [n_masks][{(V + 31) // 32}]")
         n_masks = mask.shape[0]
-    _sizes(who, hist_start=(hist_start, B + 1), bias_start=(bias_start, B + 1), prompt_len=(prompt_len, B),
-           mask_row=(mask_row, B), repetition=(repetition, B), frequency=(frequency, B), presence=(presence, B),
-           bias_vals=(bias_vals, n_bias))
+    if not ((hist is None or (_is(hist, _I32, dev, n_hist) and _is(hist_start, _I32, dev, B + 1)))
+            and (bias_ids is None or (_is(bias_ids, _I32, dev, n_bias) and _is(bias_vals, _F32, dev, n_bias)
+                                      and _is(bias_start, _I32, dev, B + 1)))
+            and (prompt_len is None or _is(prompt_len, _I32, dev, B))
+            and (repetition is None or _is(repetition, _F32, dev, B))
+            and (frequency is None or _is(frequency, _F32, dev, B))
+            and (presence is None or _is(presence, _F32, dev, B))
+            and (mask is None or (mask.dtype is _I32 and mask.get_device() == dev and mask.is_contiguous()))
+            and (mask_row is None or _is(mask_row, _I32, dev, B))):
+        _dense(who, dev, _I32, hist=hist, hist_start=hist_start, prompt_len=prompt_len, bias_ids=bias_ids,
+               bias_start=bias_start, mask=mask, mask_row=mask_row)
+        _dense(who, dev, _F32, repetition=repetition, frequency=frequency, presence=presence, bias_vals=bias_vals)
+        _sizes(who, hist_start=(hist_start, B + 1), bias_start=(bias_start, B + 1), prompt_len=(prompt_len, B),
+               mask_row=(mask_row, B), repetition=(repetition, B), frequency=(frequency, B), presence=(presence, B),
+               bias_vals=(bias_vals, n_bias))
     if B == 0 or V == 0:
         return
     a = bc_logits_args(logits.data_ptr(), out.data_ptr(), dt, B, V, logits.stride(0) if B > 1 else V,
@@ -245,6 +276,7 @@ class RaggedCache:
         self.layers, self.batch, self.group, self.max_q, self.code = layers, batch, group, max_q, code
         ints = lambda *s: torch.zeros(*s, dtype=torch.int32, device=device)
         self.pool = torch.empty(layers, n_pages, n_kv_heads, 32 * head_dim + 32, dtype=torch.uint8, device=device)
+        self._pools = self.pool.unbind(0)
         self.table, self.lens, self.q_start = ints(batch, max_blocks), ints(batch), ints(batch + 1)
         self.free_list = torch.arange(n_pages, dtype=torch.int32, device=device)
         self.n_free = ints(1).fill_(n_pages)
@@ -263,12 +295,13 @@ class RaggedCache:
         n = k.shape[0]
         if n > self.slots.numel():
             raise ValueError(f"RaggedCache.append: more than {self.slots.numel()} tokens")
-        kv8_append(k, v, self.slots[:n], self.pool[layer], self.code, stream)
+        slots = self.slots if n == self.slots.numel() else self.slots[:n]
+        kv8_append(k, v, slots, self._pools[layer], self.code, stream)
 
     def attend(self, layer: int, q, out, stream=None, **options):
         """q [n_q][Hq][hd], the queries of the step's new tokens; options as
         for kv8_attention."""
-        kv8_attention(q, self.pool[layer], self.lens, self.table, out, self.scratch, self.code, self.q_start,
+        kv8_attention(q, self._pools[layer], self.lens, self.table, out, self.scratch, self.code, self.q_start,
                       self.max_q, stream=stream, **options)
 
     def read(self, layer: int, seq: int, n: int, dtype=torch.bfloat16):
@@ -282,7 +315,7 @@ class RaggedCache:
         slots = (self.table[seq][pos // 16] * 16 + pos % 16).int()
         k = torch.empty(n, H, hd, dtype=dtype, device=dev)
         v = torch.empty_like(k)
-        kv8_gather(self.pool[layer], slots, k, v, self.code)
+        kv8_gather(self._pools[layer], slots, k, v, self.code)
         return k, v
 
     def status(self, stream=None):
