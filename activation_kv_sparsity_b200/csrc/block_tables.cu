@@ -19,14 +19,16 @@
 
 namespace bc {
 
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanItems = BC_RAGGED_MAX_BATCH / kPlanThreads;
+// Threads of a CTA: the sums of a small batch take few warps.
+constexpr int kPlanSmall = 128, kPlanLarge = 1024;
+constexpr int kPlanTokens = 2;     // tokens per thread in flight
 
 struct Sum2 {
   long long a, b;
 };
 
 // Exclusive running sums of a pair over the block; *total receives the sums.
+template <int NT>
 __device__ __forceinline__ Sum2 block_scan2(Sum2 v, Sum2* red, Sum2* total) {
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
   Sum2 x = v;
@@ -41,7 +43,7 @@ __device__ __forceinline__ Sum2 block_scan2(Sum2 v, Sum2* red, Sum2* total) {
   if (l == 31) red[w] = x;
   __syncthreads();
   if (w == 0) {
-    Sum2 t = red[l];
+    Sum2 t = l < NT / 32 ? red[l] : Sum2{0, 0};
     #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long a = __shfl_up_sync(0xffffffffu, t.a, o), b = __shfl_up_sync(0xffffffffu, t.b, o);
@@ -55,7 +57,7 @@ __device__ __forceinline__ Sum2 block_scan2(Sum2 v, Sum2* red, Sum2* total) {
   __syncthreads();
   Sum2 before = {0, 0};
   if (w > 0) before = red[w - 1];
-  *total = red[kPlanThreads / 32 - 1];
+  *total = red[NT / 32 - 1];
   __syncthreads();
   return Sum2{before.a + x.a - v.a, before.b + x.b - v.b};
 }
@@ -73,7 +75,8 @@ __device__ __forceinline__ int find_seq(const int* sums, int n, int x) {
 
 __device__ __forceinline__ int pages_of(long long n) { return (int)((n + kPage - 1) / kPage); }
 
-__global__ void __launch_bounds__(kPlanThreads) k_block_tables(bc_block_tables_args a) {
+template <int NT, int ITEMS>
+__global__ void __launch_bounds__(NT) k_block_tables(const __grid_constant__ bc_block_tables_args a) {
   extern __shared__ int sm[];
   const int B = a.batch;
   int* s_len = sm;                 // [B] tokens held
@@ -87,11 +90,11 @@ __global__ void __launch_bounds__(kPlanThreads) k_block_tables(bc_block_tables_a
 
   const long long cap = (long long)a.max_blocks * kPage;
   const int n_free = min(max(*a.n_free, 0), a.n_pages);
-  long long len[kPlanItems], now[kPlanItems], cand[kPlanItems], need[kPlanItems], back[kPlanItems];
+  long long len[ITEMS], now[ITEMS], cand[ITEMS], need[ITEMS], back[ITEMS];
   Sum2 mine = {0, 0}, total;
   #pragma unroll
-  for (int i = 0; i < kPlanItems; ++i) {
-    const int b = threadIdx.x * kPlanItems + i;
+  for (int i = 0; i < ITEMS; ++i) {
+    const int b = threadIdx.x * ITEMS + i;
     len[i] = now[i] = cand[i] = need[i] = back[i] = 0;
     if (b < B) {
       const long long d = a.delta[b];
@@ -103,15 +106,15 @@ __global__ void __launch_bounds__(kPlanThreads) k_block_tables(bc_block_tables_a
     mine.a += cand[i];
     mine.b += back[i];
   }
-  const Sum2 s1 = block_scan2(mine, red, &total);
+  const Sum2 s1 = block_scan2<NT>(mine, red, &total);
   const long long n_back = total.b;
   // at most n_pages free pages (more would mean a page held twice)
   const int room = (int)min(n_free + n_back, (long long)a.n_pages);
   long long at = s1.a, rel = s1.b;
   mine.a = mine.b = 0;
   #pragma unroll
-  for (int i = 0; i < kPlanItems; ++i) {
-    const int b = threadIdx.x * kPlanItems + i;
+  for (int i = 0; i < ITEMS; ++i) {
+    const int b = threadIdx.x * ITEMS + i;
     at += cand[i];
     if (at > a.max_tokens) cand[i] = 0;
     need[i] = cand[i] ? pages_of(len[i] + cand[i]) - pages_of(len[i]) : 0;
@@ -119,22 +122,22 @@ __global__ void __launch_bounds__(kPlanThreads) k_block_tables(bc_block_tables_a
     if (b < B) s_back[b] = (int)min(rel, (long long)a.n_pages + 1);
     rel += back[i];
   }
-  const Sum2 s2 = block_scan2(mine, red, &total);
+  const Sum2 s2 = block_scan2<NT>(mine, red, &total);
   at = s2.a;
   mine.a = mine.b = 0;
   #pragma unroll
-  for (int i = 0; i < kPlanItems; ++i) {
+  for (int i = 0; i < ITEMS; ++i) {
     at += need[i];
     if (need[i] && at > room) cand[i] = need[i] = 0;
     mine.a += cand[i];
     mine.b += need[i];
   }
-  const Sum2 s3 = block_scan2(mine, red, &total);
+  const Sum2 s3 = block_scan2<NT>(mine, red, &total);
   const int n_tok = (int)total.a, n_take = (int)total.b;
   long long tok = s3.a, take = s3.b;
   #pragma unroll
-  for (int i = 0; i < kPlanItems; ++i) {
-    const int b = threadIdx.x * kPlanItems + i;
+  for (int i = 0; i < ITEMS; ++i) {
+    const int b = threadIdx.x * ITEMS + i;
     if (b < B) {
       s_len[b] = (int)len[i];
       s_start[b] = (int)tok;
@@ -160,25 +163,33 @@ __global__ void __launch_bounds__(kPlanThreads) k_block_tables(bc_block_tables_a
     const int kept = pages_of(s_len[b]) - (s_back[b + 1] - s_back[b]);
     return a.table[(size_t)b * a.max_blocks + kept + (r - s_back[b])];
   };
-  const int t0 = blockIdx.x * kPlanThreads + threadIdx.x, step = gridDim.x * kPlanThreads;
+  const int t0 = blockIdx.x * NT + threadIdx.x, step = gridDim.x * NT;
+  for (long long i0 = t0; i0 < a.max_tokens; i0 += (long long)kPlanTokens * step) {
+    int pos[kPlanTokens], page[kPlanTokens];
+    #pragma unroll
+    for (int j = 0; j < kPlanTokens; ++j) {
+      const long long i = i0 + (long long)j * step;
+      pos[j] = page[j] = -1;
+      if (i < n_tok) {
+        const int b = find_seq(s_start, B, (int)i);
+        pos[j] = s_len[b] + (int)i - s_start[b];
+        const int blk = pos[j] / kPage, held = pages_of(s_len[b]);
+        page[j] = blk < held ? a.table[(size_t)b * a.max_blocks + blk] : free_page(room - 1 - (s_take[b] + blk - held));
+      }
+    }
+    #pragma unroll
+    for (int j = 0; j < kPlanTokens; ++j) {
+      const long long i = i0 + (long long)j * step;
+      if (i >= a.max_tokens) break;
+      a.slots[i] = page[j] >= 0 && page[j] < a.n_pages ? page[j] * kPage + pos[j] % kPage : -1;
+      a.positions[i] = pos[j];
+    }
+  }
   for (int j = t0; j < n_take; j += step) {
     const int b = find_seq(s_take, B, j);
     a.table[(size_t)b * a.max_blocks + pages_of(s_len[b]) + (j - s_take[b])] = free_page(room - 1 - j);
   }
   for (int x = n_free + t0; x < room - n_take; x += step) a.free_list[x] = free_page(x);
-  for (long long i = t0; i < a.max_tokens; i += step) {
-    int slot = -1, pos = -1;
-    if (i < n_tok) {
-      const int b = find_seq(s_start, B, (int)i);
-      pos = s_len[b] + (int)i - s_start[b];
-      const int blk = pos / kPage, held = pages_of(s_len[b]);
-      const int page = blk < held ? a.table[(size_t)b * a.max_blocks + blk]
-                                  : free_page(room - 1 - (s_take[b] + blk - held));
-      if (page >= 0 && page < a.n_pages) slot = page * kPage + pos % kPage;
-    }
-    a.slots[i] = slot;
-    a.positions[i] = pos;
-  }
 
   // every CTA has read its inputs once the last one is here
   __syncthreads();
@@ -190,8 +201,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_block_tables(bc_block_tables_a
   __syncthreads();
   if (!s_last) return;
   #pragma unroll
-  for (int i = 0; i < kPlanItems; ++i) {
-    const int b = threadIdx.x * kPlanItems + i;
+  for (int i = 0; i < ITEMS; ++i) {
+    const int b = threadIdx.x * ITEMS + i;
     if (b < B) a.lens_out[b] = (int)now[i];
   }
   if (threadIdx.x == 0) {
@@ -217,9 +228,13 @@ extern "C" bc_status bc_block_tables(const bc_block_tables_args* a, void* stream
     return entry_fail(BC_EINVAL, "bc_block_tables: bad n_pages %d", a->n_pages);
   if (a->max_tokens < 0) return entry_fail(BC_EINVAL, "bc_block_tables: max_tokens < 0");
   const size_t smem = 4ull * (4 * (size_t)a->batch + 3);
-  // 2 tokens a thread: the sums cost every CTA the same, so more CTAs only
-  // shorten the token loop
-  const int grid = std::min(148, std::max(1, (int)((a->max_tokens + 2LL * kPlanThreads - 1) / (2 * kPlanThreads))));
-  return entry_cuda(launch_op(k_block_tables, dim3(grid), dim3(kPlanThreads), smem, static_cast<cudaStream_t>(stream),
-                              *a), "bc_block_tables");
+  // kPlanTokens tokens a thread: the sums cost every CTA the same, so more
+  // CTAs only shorten the token loop
+  const int nt = a->batch <= kPlanSmall && a->max_tokens <= 4 * kPlanSmall ? kPlanSmall : kPlanLarge;
+  const long long per = (long long)nt * kPlanTokens;
+  const dim3 grid((unsigned)std::min(148LL, std::max(1LL, (a->max_tokens + per - 1) / per)));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return entry_cuda(nt == kPlanSmall ? launch_op(k_block_tables<kPlanSmall, 1>, grid, dim3(nt), smem, st, *a)
+                                     : launch_op(k_block_tables<kPlanLarge, BC_RAGGED_MAX_BATCH / kPlanLarge>, grid,
+                                                 dim3(nt), smem, st, *a), "bc_block_tables");
 }
