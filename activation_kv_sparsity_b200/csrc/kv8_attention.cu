@@ -19,7 +19,7 @@
 // A segment that lies in one worker's piece goes straight to the output.
 // Pieces of a segment are merged in shared memory within a CTA, and through
 // the scratch between CTAs, by the last of them to finish (an atomic ticket
-// per pair, no spinning).  All merges run in a fixed order.
+// per segment, kept by the CTA it begins in; no spinning).  All merges run in a fixed order.
 //
 // Products on mma.sync m16n8k16 with f16 operands (both code types are exact
 // in f16), the cache as the A operand and the 8 rows as its 8 columns, so no
@@ -63,7 +63,7 @@ struct Attn8Args {
   int nt, nt_log2;        // warps per worker
   int rows;               // group * max_q
   float* part;            // [grid][2][rows][HD + 4] partials between CTAs
-  unsigned* tickets;      // [batch * n_kv_heads], zero between calls
+  unsigned* tickets;      // [kA8MaxCtas] of the segment that begins in a CTA and goes on, zero between calls
   unsigned* status;       // bit 0: a wait gave up
 };
 
@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     bool last = false;
     if (s_nout >> tid & 1) {
       const Cut& c = s_cut[s_out_cut[tid]];
-      unsigned* ticket = ga.tickets + (size_t)c.b * H + c.h;
+      unsigned* ticket = ga.tickets + c.s0 / per_cta;
       unsigned prev;
       asm volatile("atom.add.acq_rel.gpu.u32 %0, [%1], 1;" : "=r"(prev) : "l"(ticket) : "memory");
       last = prev == (unsigned)((c.s1 - 1) / per_cta - c.s0 / per_cta);
@@ -823,17 +823,11 @@ static bool attn8_sizes_ok(int batch, int H, int group, int max_q, int hd) {
          max_q <= 64 && group * max_q <= 64 && (hd == 64 || hd == 128);
 }
 
-// Scratch: the status word, the tickets, the partials between CTAs.
-struct Attn8Layout {
-  size_t tickets, part, total;
-};
-static Attn8Layout attn8_layout(int batch, int H, int rows, int hd) {
-  Attn8Layout y;
-  y.tickets = 256;
-  y.part = y.tickets + ((4ull * batch * H + 255) & ~255ull);
-  y.total = y.part + 4ull * kA8MaxCtas * 2 * rows * (hd + 4);
-  return y;
-}
+// Scratch: the status word, the tickets, the partials between CTAs.  The words
+// that have to be zero lie in the same place whatever the sizes are, so calls
+// of different sizes can share a scratch.
+constexpr size_t kA8TicketsAt = 256, kA8PartAt = 1024;
+static_assert(kA8TicketsAt + 4 * kA8MaxCtas <= kA8PartAt, "tickets overlap the partials");
 
 template <int HD, int TYPE, bool SPLIT, bool MODS>
 static cudaError_t attn8_launch(const Attn8Args& g, int grid, cudaStream_t st) {
@@ -855,7 +849,7 @@ static cudaError_t attn8_launch(const Attn8Args& g, int grid, cudaStream_t st) {
 
 extern "C" size_t bc_kv8_attention_scratch_bytes(int batch, int n_kv_heads, int group, int max_q, int head_dim) {
   if (!attn8_sizes_ok(batch, n_kv_heads, group, max_q, head_dim)) return 0;
-  return attn8_layout(batch, n_kv_heads, group * max_q, head_dim).total;
+  return kA8PartAt + 4ull * kA8MaxCtas * 2 * group * max_q * (head_dim + 4);
 }
 
 extern "C" bc_status bc_kv8_attention(const bc_kv8_attention_args* a, void* stream) {
@@ -896,11 +890,10 @@ extern "C" bc_status bc_kv8_attention(const bc_kv8_attention_args* a, void* stre
   g.nt_log2 = 0;
   while ((8 << g.nt_log2) < g.rows) ++g.nt_log2;
   g.nt = 1 << g.nt_log2;
-  const Attn8Layout y = attn8_layout(a->batch, a->n_kv_heads, g.rows, a->head_dim);
   char* sc = static_cast<char*>(a->scratch);
   g.status = reinterpret_cast<unsigned*>(sc);
-  g.tickets = reinterpret_cast<unsigned*>(sc + y.tickets);
-  g.part = reinterpret_cast<float*>(sc + y.part);
+  g.tickets = reinterpret_cast<unsigned*>(sc + kA8TicketsAt);
+  g.part = reinterpret_cast<float*>(sc + kA8PartAt);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

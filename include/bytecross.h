@@ -526,7 +526,8 @@ BC_API bc_status bc_kv8_gather(const void* pool, bc_kv8_type type, int n_pages, 
  *            first n_sel[b] of each row used; others of a row are skipped
  *   scratch  bc_kv8_attention_scratch_bytes(...) bytes, 256-byte aligned:
  *            partial results, a status word and tickets; zero it before the
- *            first call.  Calls that may overlap on the GPU need one each.
+ *            first call (every call leaves the tickets at zero).  Calls of any
+ *            sizes can share it, calls that may overlap on the GPU not.
  * Lengths outside [0, 16 max_blocks] are taken as the nearest bound.
  * max_blocks <= 2^25, n_q <= 2^29, and n_pages * n_kv_heads and batch *
  * n_kv_heads * (the larger of max_blocks and, with pages, max_sel) are at most

@@ -601,3 +601,116 @@ def test_logits_long_lists(hist, bias):
         out = src if out is None else out
         bc.logits_adjust(src, out, **{k: to(DEV, v) for k, v in kw.items()})
         assert np.abs(out.cpu().double().numpy() - want).max() <= 5 * 2.0 ** -24 * 20
+
+
+def attention_inputs(lens, H, G, hd, code, seed=0):
+    """(q, pool, lens, table, definition) of one query a sequence."""
+    blocks = [og.pages_of(n) for n in lens]
+    pool = make_pool(sum(blocks) + 1, H, hd, code, seed=seed)
+    table = np.full((len(lens), max(blocks) + 1), -1, np.int32)
+    at = 0
+    for b, n in enumerate(blocks):
+        table[b, :n] = np.arange(at, at + n)[::-1]
+        at += n
+    q = torch.randn(len(lens), H * G, hd, generator=gen(seed + 1))
+    want = og.attention(q.numpy(), pool, lens, table, code, hd)
+    tol = attention_tol(want, q.double().numpy(), pool, code, hd, max(lens), 0.0, None, False)
+    return q.to(DEV), to(DEV, pool), ints(lens), ints(table), want, tol
+
+
+def test_attention_calls_of_any_sizes_share_a_scratch():
+    cases = [([3000], 1, 8, 64, "int8"), ([700, 90, 16] * 5, 3, 2, 128, "e4m3"), ([5], 1, 1, 64, "e4m3"),
+             ([2000, 1, 400], 4, 8, 128, "int8")]
+    need = max(bc.bc_kv8_attention_scratch_bytes(len(l), H, G, 1, hd) for l, H, G, hd, _ in cases)
+    scratch = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    made = [(c, attention_inputs(*c, seed=i)) for i, c in enumerate(cases)]
+    for _ in range(2):
+        for (lens, H, G, hd, code), (q, pool, ld, table, want, tol) in made:
+            out = torch.empty_like(q)
+            bc.kv8_attention(q, pool, ld, table, out, scratch, code)
+            assert (np.abs(out.cpu().double().numpy() - want) <= tol).all()
+
+
+def test_two_streams_at_once():
+    """Calls that overlap, each with a scratch of its own, and a plan beside them."""
+    made = [attention_inputs([2500, 30, 700], 2, 4, 128, "e4m3", seed=i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    scratch = [torch.zeros(bc.bc_kv8_attention_scratch_bytes(3, 2, 4, 1, 128), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    outs = [[torch.empty_like(m[0]) for _ in range(20)] for m in made]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for s in range(2):
+            q, pool, ld, table, _, _ = made[s]
+            bc.kv8_attention(q, pool, ld, table, outs[s][i], scratch[s], "e4m3", stream=streams[s])
+    torch.cuda.synchronize()
+    for s in range(2):
+        for o in outs[s]:
+            assert torch.equal(o, outs[s][0])
+        assert (np.abs(outs[s][0].cpu().double().numpy() - made[s][4]) <= made[s][5]).all()
+
+
+def test_wrappers_say_what_is_wrong():
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32, device=DEV)
+    f = lambda *s, **k: torch.zeros(*s, device=DEV, **k)
+    pool = torch.zeros(4, 2, 32 * 64 + 32, dtype=torch.uint8, device=DEV)
+    x = f(3, 2, 64)
+
+    def refused(what, fn, *args, **kw):
+        with pytest.raises(ValueError, match=what):
+            fn(*args, **kw)
+
+    for bad in (i(3).long(), i(6)[::2], i(3).cpu(), i(2)):
+        refused("slots|k must be", bc.kv8_append, x, x, bad, pool)
+        refused("slots|k_out must be", bc.kv8_gather, pool, bad, x, x)
+    refused("v must be", bc.kv8_append, x, x.to(torch.bfloat16), i(3), pool)
+    refused("float32 or bfloat16", bc.kv8_append, x.half(), x.half(), i(3), pool)
+    refused("k must be", bc.kv8_append, f(3, 64, 2).transpose(1, 2).contiguous()[:, :, :63], x, i(3), pool)
+    refused("dense", bc.kv8_append, f(3, 64, 2).transpose(1, 2), x, i(3), pool)
+    refused("code", bc.kv8_append, x, x, i(3), pool, "fp4")
+    refused("pool", bc.kv8_append, x, x, i(3), pool[:, :, :2000])
+    refused("pool", bc.kv8_append, x, x, i(3), pool[::2])
+    refused("contiguous", bc.kv8_gather, pool, i(3), f(6, 2, 64)[::2], x)
+    sc = torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)
+    q, lens, table = f(3, 8, 64), i(3), i(3, 4)
+    ok = lambda **k: bc.kv8_attention(**{**dict(q=q, pool=pool, lens=lens, table=table, out=f(3, 8, 64), scratch=sc), **k})
+    ok()
+    refused("lens", ok, lens=i(4))
+    refused("table", ok, table=i(12))
+    refused("table", ok, table=i(3, 4).float())
+    refused("out", ok, out=f(3, 8, 64, dtype=torch.bfloat16))
+    refused("out", ok, out=f(3, 8, 128)[:, :, ::2])
+    refused("q must be", ok, q=f(3, 7, 64))
+    refused("heads and dims of q", ok, q=f(3, 64, 8).transpose(1, 2))
+    refused("one query row", ok, max_q=2)
+    refused("q_start", ok, q_start=i(3), max_q=2)
+    refused("go together", ok, pages=i(3, 2, 4))
+    refused("pages must be", ok, pages=i(3, 1, 4), n_sel=i(3))
+    refused("slopes", ok, slopes=f(7))
+    refused("scratch", ok, scratch=sc.float())
+    with pytest.raises(bc.BCError):
+        ok(scratch=sc[:4096])                            # too small
+    with pytest.raises(bc.BCError):
+        ok(q=f(3 * 8 * 64 + 2)[2:].view(3, 8, 64))       # not 16-byte aligned
+    with pytest.raises(bc.BCError):
+        ok(q=f(3, 8 * 64 + 4)[:, :512].view(3, 8, 64))   # a row stride that is not a multiple of 8
+    with pytest.raises(bc.BCError):
+        ok(window=-1)
+    with pytest.raises(bc.BCError):
+        bc.kv8_append(f(3, 130)[:, :128].view(3, 2, 64), x, i(3), pool)
+    lg = f(2, 50)
+    refused("out must", bc.logits_adjust, lg, f(2, 51))
+    refused("dense", bc.logits_adjust, f(50, 2).t(), lg)
+    refused("go together", bc.logits_adjust, lg, lg, hist=i(3))
+    refused("hist_start", bc.logits_adjust, lg, lg, hist=i(3), hist_start=i(2))
+    refused("bias_vals", bc.logits_adjust, lg, lg, bias_ids=i(3), bias_vals=f(2), bias_start=i(3))
+    refused("repetition", bc.logits_adjust, lg, lg, repetition=f(3))
+    refused("mask must be", bc.logits_adjust, lg, lg, mask=i(2, 1))
+    refused("mask_row", bc.logits_adjust, lg, lg, mask_row=i(2))
+    with pytest.raises(bc.BCError):
+        bc.logits_adjust(lg, lg, mask=i(1, 2))           # two rows, one mask
+    t = dict(lens=i(2), delta=i(2), table=i(2, 3), free_list=i(5), n_free=i(1), lens_out=i(2), n_free_out=i(1),
+             q_start=i(3), slots=i(4), positions=i(4), ticket=i(1))
+    bc.block_tables(**t)
+    for k, v in dict(lens=i(3), q_start=i(2), positions=i(3), n_free=i(2), delta=i(2).float(), free_list=i(10)[::2]).items():
+        refused(k, bc.block_tables, **{**t, k: v})
+    torch.cuda.synchronize()
