@@ -7,19 +7,23 @@
 // bytes of its pages: 1 byte per key or value element read once, at most 128
 // flops for it, so HBM bounds it.
 //
-// Work split.  The pages of all (sequence, kv head) pairs, in that order, are
-// one line of units; it is cut into equal pieces, one per worker, whatever
-// the lengths are: a worker's piece may begin and end inside a sequence and
-// hold several.  A CTA (one per SM) has 16 warps; a warp takes 8 query rows,
-// and the NT warps that share a sequence's rows form a worker and share its
-// pages.  A worker reads its pages through a ring in shared memory, filled by
-// bulk copies (a block of a page and head, scales included, is contiguous)
-// 2 NT pages ahead, 32 blocks per SM; the page numbers come from registers,
-// 64 units ahead.
-// A segment that lies in one worker's piece goes straight to the output.
+// Work split.  A segment is the pages of one (sequence, kv head, 8 query
+// rows); the pages of all segments, in that order, are one line of units; it
+// is cut into equal pieces, one per warp, whatever the lengths are: a warp's
+// piece may begin and end inside a segment and hold several.  A CTA (one per
+// SM) has 16 warps.  A warp reads its pages through a ring in shared memory,
+// filled by bulk copies (a block of a page and head, scales included, is
+// contiguous) 2 pages ahead, 32 blocks per SM; the page numbers come from
+// registers, 64 units ahead.  Sequences with more than 8 rows (several
+// queries, or drafts) have their blocks read once per 8 rows, mostly from L2;
+// the products, not the bytes, bound those (sharing a block between the warps
+// of a sequence's rows left warps idle where sequences differ in queries:
+// 55 us for 16 sequences with 1 to 4 drafts in a window of 4096 tokens).
+// A segment that lies in one warp's piece goes straight to the output.
 // Pieces of a segment are merged in shared memory within a CTA, and through
 // the scratch between CTAs, by the last of them to finish (an atomic ticket
-// per segment, kept by the CTA it begins in; no spinning).  All merges run in a fixed order.
+// per segment, kept by the CTA it begins in; no spinning).  All merges run in
+// a fixed order.
 //
 // Products on mma.sync m16n8k16 with f16 operands (both code types are exact
 // in f16), the cache as the A operand and the 8 rows as its 8 columns, so no
@@ -54,15 +58,14 @@
 namespace bc {
 
 constexpr int kA8Warps = 16, kA8Threads = kA8Warps * 32;
-constexpr int kA8Stages = 2 * kA8Warps;   // blocks in flight per CTA
+constexpr int kA8Ring = 2;          // blocks in flight per warp
+constexpr int kA8Rows = 8;          // query rows per segment
 constexpr int kA8MaxCtas = 160;     // CTAs the scratch provides for
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Attn8Args {
   bc_kv8_attention_args a;
-  int nt, nt_log2;        // warps per worker
-  int rows;               // group * max_q
-  float* part;            // [grid][2][rows][HD + 4] partials between CTAs
+  float* part;            // [grid][2][8][HD + 4] partials between CTAs
   unsigned* tickets;      // [kA8MaxCtas] of the segment that begins in a CTA and goes on, zero between calls
   unsigned* status;       // bit 0: a wait gave up
 };
@@ -128,7 +131,8 @@ __device__ __forceinline__ float cap_logit(float x, float cap, float inv_cap) {
 
 // A segment as its flush and its masks need it.
 struct Segment {
-  int h, begin, r0, rows;    // kv head, first unit, first query row, rows
+  int h, begin, r0;          // kv head, first unit, the sequence's first query row
+  int row0, rows;            // its first row of the sequence's, and their end
   int first, last;           // positions of its first and last query
 };
 
@@ -141,6 +145,7 @@ struct Seq {
   int n;          // tokens
   int r0, own;    // first query row, its queries
   int lo, cnt;    // first page (without a list), pages (entries of the list)
+  int rows;       // query rows of a kv head, max_q queries at most
 };
 
 __device__ __forceinline__ Seq seq_of(const bc_kv8_attention_args& a, int n, int r0, int own, int b) {
@@ -149,12 +154,13 @@ __device__ __forceinline__ Seq seq_of(const bc_kv8_attention_args& a, int n, int
   s.r0 = r0;
   s.own = max(own, 0);
   s.lo = s.cnt = 0;
-  const int rows = min(s.own, a.max_q);
-  if (rows == 0) return s;
+  const int queries = min(s.own, a.max_q);
+  s.rows = queries * a.group;
+  if (queries == 0) return s;
   if (a.pages) {
     s.cnt = clampi(a.n_sel[b], 0, a.max_sel);
   } else {
-    const int first = n - s.own, last = first + rows - 1;   // positions of the first and last query
+    const int first = n - s.own, last = first + queries - 1;   // positions of the first and last query
     if (a.window > 0) s.lo = max(0, first - a.window + 1) / kPage;
     s.cnt = last < 0 ? 0 : max(0, last / kPage + 1 - s.lo);
   }
@@ -166,31 +172,24 @@ __device__ __forceinline__ Seq seq_of(const bc_kv8_attention_args& a, int n, int
 template <int HD, int TYPE, bool SPLIT, bool MODS>
 __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constant__ Attn8Args ga) {
   constexpr int BLK = kv8_block_bytes(HD);
-  constexpr int ROWS = 8;                  // query rows per warp
   constexpr int U = HD / 64, V4 = HD / 32;
   constexpr int SROW = HD + 4;             // a partial's row: o, then m, l, mo
   const bc_kv8_attention_args& a = ga.a;
-  const int B = a.batch, H = a.n_kv_heads, G = a.group, NT = ga.nt;
-  const int GP = kA8Warps >> ga.nt_log2;                // workers per CTA
-  const int s_log2 = 1 + ga.nt_log2, S = 1 << s_log2;   // ring stages per worker
+  const int B = a.batch, H = a.n_kv_heads, G = a.group;
 
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* ring = smem;
-  float* heads = reinterpret_cast<float*>(smem + kA8Stages * BLK);          // [GP][NT * ROWS][SROW]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(heads + kA8Warps * ROWS * SROW);   // full, then empty
-  int* s_cum = reinterpret_cast<int*>(bars + 2 * kA8Stages);                // [B + 1] running sum of the pages
+  uint8_t* ring = smem;                                                     // [warps][kA8Ring] blocks
+  float* heads = reinterpret_cast<float*>(smem + kA8Warps * kA8Ring * BLK); // [warps][kA8Rows][SROW]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(heads + kA8Warps * kA8Rows * SROW);
+  int* s_cum = reinterpret_cast<int*>(bars + kA8Warps * kA8Ring);           // [B + 1] running sum of pages x tiles
   int* s_len = s_cum + B + 1;                                               // [B]
   int* s_row = s_len + B;                                                   // [B + 1] first query rows
   __shared__ int s_red[32];
   __shared__ int s_last[2];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int worker = warp >> ga.nt_log2, wt = warp & (NT - 1);
-  const uint32_t full0 = smem_addr(bars) + 8 * worker * S, empty0 = full0 + 8 * kA8Stages;
-  if (tid < kA8Stages) {
-    mbar_init(smem_addr(bars) + 8 * tid, 1);
-    mbar_init(smem_addr(bars) + 8 * (kA8Stages + tid), NT);
-  }
+  const uint32_t full0 = smem_addr(bars) + 8 * warp * kA8Ring;
+  if (tid < kA8Warps * kA8Ring) mbar_init(smem_addr(bars) + 8 * tid, 1);
   if (tid == 0) mbar_init_fence();
   pdl_wait();
   pdl_trigger();
@@ -208,9 +207,10 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
       s_len[b] = n;
       s_row[b] = r0;
       if (b == B - 1) s_row[B] = r0 + own;
-      const int cnt = seq_of(a, n, r0, own, b).cnt;
-      s_cum[b] = cnt;
-      mine += cnt;
+      const Seq s = seq_of(a, n, r0, own, b);
+      const int units = s.cnt * ((s.rows + kA8Rows - 1) / kA8Rows);
+      s_cum[b] = units;
+      mine += units;
     }
   }
   int T;
@@ -218,9 +218,9 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   for (int i = 0; i < ipt; ++i) {
     const int b = tid * ipt + i;
     if (b < B) {
-      const int cnt = s_cum[b];
+      const int units = s_cum[b];
       s_cum[b] = run;
-      run += cnt;
+      run += units;
     }
   }
   if (tid == 0) s_cum[B] = T;
@@ -242,16 +242,17 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   }
 
   const int total = T * H;
-  const int per = max(1, (int)(((unsigned)total + gridDim.x * GP - 1) / (gridDim.x * GP)));   // units per worker
-  const int per_cta = per * GP;
+  const int per = max(1, (int)(((unsigned)total + gridDim.x * kA8Warps - 1) / (gridDim.x * kA8Warps)));   // units per warp
+  const int per_cta = per * kA8Warps;
   const int c0 = (int)min((long long)blockIdx.x * per_cta, (long long)total);
   const int c1 = (int)min((long long)c0 + per_cta, (long long)total);
   if (c0 >= c1) return;
-  const int g0 = (int)min((long long)c0 + (long long)worker * per, (long long)c1);
+  const int g0 = (int)min((long long)c0 + (long long)warp * per, (long long)c1);
   const int g1 = (int)min((long long)g0 + per, (long long)c1);
 
-  // the pair (b, h) that unit u belongs to, and the units of that pair
-  auto locate = [&](int u, int& b, int& h, int& begin, int& end) {
+  auto seq_at = [&](int b) { return seq_of(a, s_len[b], s_row[b], s_row[b + 1] - s_row[b], b); };
+  // the segment of unit u: sequence, kv head, 8 rows, units
+  auto locate = [&](int u, int& b, int& h, int& tile, int& begin, int& end) {
     const int x = (unsigned)u / (unsigned)H;
     int lo = 0, hi = B;                      // last b with s_cum[b] <= x
     while (hi - lo > 1) {
@@ -260,12 +261,14 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
       else hi = mid;
     }
     b = lo;
-    const int cnt = s_cum[b + 1] - s_cum[b], base = s_cum[b] * H;
-    h = (unsigned)(u - base) / (unsigned)cnt;
-    begin = base + h * cnt;
+    const int tiles = (min(max(s_row[b + 1] - s_row[b], 0), a.max_q) * G + kA8Rows - 1) / kA8Rows;
+    const unsigned of_head = s_cum[b + 1] - s_cum[b], at = u - s_cum[b] * H;
+    const unsigned cnt = tiles == 1 ? of_head : of_head / (unsigned)tiles;
+    h = at / of_head;
+    tile = tiles == 1 ? 0 : (at - h * of_head) / cnt;
+    begin = s_cum[b] * H + h * of_head + tile * cnt;
     end = begin + cnt;
   };
-  auto seq_at = [&](int b) { return seq_of(a, s_len[b], s_row[b], s_row[b + 1] - s_row[b], b); };
 
   // ---- pages of the cache: lane l holds those of units base + l and base +
   // 32 + l.  A lookup only starts its loads; found() turns what came into the
@@ -274,8 +277,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     entry = logical = -1;
     const int u = g0 + k;
     if (u >= g1) return;
-    int b, h, begin, end;
-    locate(u, b, h, begin, end);
+    int b, h, tile, begin, end;
+    locate(u, b, h, tile, begin, end);
     if (a.pages) {
       logical = a.pages[((size_t)b * H + h) * a.max_sel + (u - begin)];
       if (logical < 0 || logical >= (s_len[b] + kPage - 1) / kPage) return;
@@ -285,9 +288,9 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     entry = a.table[(size_t)b * a.max_blocks + logical];
   };
   auto found = [&](int k, int& block, int& logical) {
-    int b, h, begin, end;
+    int b, h, tile, begin, end;
     if (block >= 0 && block < a.n_pages) {
-      locate(g0 + k, b, h, begin, end);
+      locate(g0 + k, b, h, tile, begin, end);
       block = block * H + h;
     } else {
       block = logical = -1;
@@ -296,20 +299,21 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   int base = 0, bl0 = -1, bl1 = -1, lg0 = -1, lg1 = -1;
 
   const int n_units = g1 - g0;
-  uint8_t* my_ring = ring + (size_t)worker * S * BLK;
-  uint64_t stream;                                // the cache is read once: first to leave L2
-  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(stream));
-  auto issue = [&](int k) {                       // by the leader warp, all lanes
+  uint8_t* my_ring = ring + warp * kA8Ring * BLK;
+  // the cache is read once: first to leave L2 (not so if it is read per 8 rows)
+  uint64_t policy;
+  if (G * a.max_q <= kA8Rows) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+  auto issue = [&](int k) {
     const int block = __shfl_sync(0xffffffffu, k - base < 32 ? bl0 : bl1, (k - base) & 31);
     if (lane == 0) {
-      const uint32_t bar = full0 + 8 * (k & (S - 1));
+      const uint32_t bar = full0 + 8 * (k & (kA8Ring - 1));
       if (block >= 0) {
         mbar_arrive_expect_tx(bar, BLK);
         asm volatile(
             "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], "
-            "%4;" ::"r"(
-                smem_addr(my_ring + (k & (S - 1)) * BLK)),
-            "l"(static_cast<const uint8_t*>(a.pool) + (size_t)block * BLK), "r"(BLK), "r"(bar), "l"(stream)
+            "%4;" ::"r"(smem_addr(my_ring + (k & (kA8Ring - 1)) * BLK)),
+            "l"(static_cast<const uint8_t*>(a.pool) + (size_t)block * BLK), "r"(BLK), "r"(bar), "l"(policy)
             : "memory");
       } else {
         mbar_arrive(bar);                         // a page that is not there
@@ -318,29 +322,27 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   };
 
   // ---- the segment at hand
-  // Lane (g, t) loads row g of each of the warp's tiles; scores, weights and
-  // outputs are of rows 2t and 2t + 1.
+  // Lane (g, t) loads row g of its queries; scores, weights and outputs are of
+  // rows 2t and 2t + 1.
   __shared__ Segment s_seg[kA8Warps];
   Segment* my_seg = s_seg + warp;
   int seg_end = g0;
   uint32_t qh[4 * U][2], ql[SPLIT ? 4 * U : 1][2];
   float o[V4][2][4];
   float m[2], l[2], mo[2], qs[2], slope[2];
-  int at[2];                              // the row's position (rows that are not there: INT32_MAX)
-  int tile_lo = 0, tile_hi = 0;               // positions every row of the warp sees
-  bool live = false;
+  int at[2];                                  // the row's position (rows that are not there: INT32_MAX)
+  int all_lo = 0, all_hi = 0;                 // positions every row sees
   int gave_up = -1;                           // a wait ran out: the pages issued until then
 
   constexpr int NRAW = SPLIT ? 4 * U : 2 * U;
   uint4 raw[NRAW];                        // query rows as loaded
   // takes up the segment of unit u and starts to load its queries
   auto begin_segment = [&](int u) {
-    int b, h, begin;
-    locate(u, b, h, begin, seg_end);
+    int b, h, tile, begin;
+    locate(u, b, h, tile, begin, seg_end);
     const Seq s = seq_at(b);
-    const int seg_rows = min(s.own, a.max_q) * G, first = s.n - s.own;
-    live = wt * ROWS < seg_rows;
-    if (lane == 0) *my_seg = Segment{h, begin, s.r0, seg_rows, first, first + min(s.own, a.max_q) - 1};
+    const int row0 = tile * kA8Rows, first = s.n - s.own;
+    if (lane == 0) *my_seg = Segment{h, begin, s.r0, row0, s.rows, first, first + min(s.own, a.max_q) - 1};
     __syncwarp();
     #pragma unroll
     for (int v = 0; v < V4; ++v)
@@ -351,20 +353,19 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     for (int i = 0; i < 2; ++i) {
       m[i] = mo[i] = kNoMax;
       l[i] = 0.f;
-      const int row = wt * ROWS + 2 * t + i;
+      const int row = row0 + 2 * t + i;
       at[i] = INT32_MAX;
-      if (row < seg_rows) {
+      if (row < s.rows) {
         at[i] = first + row / G;
         if (a.window > 0) w_lo = max(w_lo, at[i] - a.window + 1);
         w_hi = min(w_hi, at[i]);
       }
-      slope[i] = MODS && a.slopes && row < seg_rows ? a.slopes[h * G + row % G] : 0.f;
+      slope[i] = MODS && a.slopes && row < s.rows ? a.slopes[h * G + row % G] : 0.f;
     }
-    if (!live) return;
-    tile_lo = __reduce_max_sync(0xffffffffu, w_lo);
-    tile_hi = __reduce_min_sync(0xffffffffu, w_hi);
-    const int row = wt * ROWS + g, src = s.r0 + row / G;
-    const bool ok = row < seg_rows && src >= 0 && src < a.n_q;
+    all_lo = __reduce_max_sync(0xffffffffu, w_lo);
+    all_hi = __reduce_min_sync(0xffffffffu, w_hi);
+    const int row = row0 + g, src = s.r0 + row / G;
+    const bool ok = row < s.rows && src >= 0 && src < a.n_q;
     const size_t e0 = (size_t)(ok ? src : 0) * a.q_stride + (size_t)(ok ? h * G + row % G : 0) * HD + 16 * t;
     #pragma unroll
     for (int i = 0; i < NRAW; ++i) {
@@ -376,7 +377,6 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   };
   // turns the loaded queries into operands
   auto take_queries = [&]() {
-    if (!live) return;
     float x[16 * U];
     uint32_t top = 0;
     #pragma unroll
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     }
     // this lane's scores: rows 2t + i, tokens 4 (g / 2) + 2j + g % 2
     const int pos0 = lp * kPage, pos = pos0 + 4 * (g >> 1) + (g & 1);
-    const bool whole = pos0 >= tile_lo && pos0 + kPage - 1 <= tile_hi;
+    const bool whole = pos0 >= all_lo && pos0 + kPage - 1 <= all_hi;
     float c[2][2], y[2][2];
     bool passed = false;
     #pragma unroll
@@ -513,9 +513,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
         #pragma unroll
         for (int j = 0; j < 2; ++j)
           if (c[i][j] == -INFINITY) w[i][j] = 0.f;
-      // value codes of tokens that no row of the segment sees may be any
-      // bytes: zero them where this lane reads them (the worker's other warps
-      // write the same)
+      // value codes of tokens that no query sees may be any bytes: zero them
+      // where this lane reads them
       const int any_lo = a.window > 0 ? my_seg->first - a.window + 1 : 0, any_hi = my_seg->last;
       uint32_t keep = 0xffffffffu;
       #pragma unroll
@@ -568,7 +567,6 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   };
   // the warp's rows: to a partial's rows at dst, or (dst null) to the output
   auto flush = [&](float* dst) {
-    if (!live) return;
     const Segment s = *my_seg;
     #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -577,7 +575,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
       ll += __shfl_xor_sync(0xffffffffu, ll, 8);
       ll += __shfl_xor_sync(0xffffffffu, ll, 16);
       if (gave_up >= 0) ll = __uint_as_float(0x7fc00000u);
-      const int row = wt * ROWS + 2 * t + i;
+      const int in = 2 * t + i, row = s.row0 + in;
       const float f = final_factor(m[i], ll, mo[i]);
       const int src = s.r0 + row / G;
       const bool ok = row < s.rows && src >= 0 && src < a.n_q;
@@ -585,11 +583,11 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
       for (int v = 0; v < V4; ++v) {
         const float4 y = make_float4(o[v][0][i], o[v][0][2 + i], o[v][1][i], o[v][1][2 + i]);
         const int d = 4 * (8 * v + g);
-        if (dst) *reinterpret_cast<float4*>(dst + (size_t)row * SROW + d) = y;
+        if (dst) *reinterpret_cast<float4*>(dst + in * SROW + d) = y;
         else if (ok) put(src, s.h * G + row % G, d, make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
       }
       if (dst && g == 0) {
-        float* ml = dst + (size_t)row * SROW + HD;
+        float* ml = dst + in * SROW + HD;
         ml[0] = m[i];
         ml[1] = ll;
         ml[2] = mo[i];
@@ -597,15 +595,16 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     }
     __syncwarp();
   };
-  float* my_head = heads + (size_t)worker * NT * ROWS * SROW;
+  float* my_head = heads + warp * kA8Rows * SROW;
 
-  // Segments cut between workers of this CTA, or between CTAs.  A cut
-  // segment's pieces here: the tail of the worker it begins in (or the head
-  // of worker 0 if it began in another CTA), then the heads of the next.
-  // Lane w + 1 looks at worker w's last segment, lane 0 at the CTA's first,
+  // Segments cut between warps of this CTA, or between CTAs.  A cut segment's
+  // pieces here: the tail of the warp it begins in (or the head of warp 0 if
+  // it began in another CTA), then the heads of the next.  Lane w + 1 looks at
+  // warp w's last segment, lane 0 at the CTA's first,
   // while the first pages are on their way.
   struct Cut {
-    int b, h, s0, s1, first, last, rows;
+    int b, h, s0, s1, first, last;   // segment, its units, the warps that hold pieces
+    int row0, rows;                  // its first row, and how many
     bool from_tail;
   };
   __shared__ Cut s_cut[kA8Warps + 1];
@@ -616,13 +615,15 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
       const int e0 = (int)min((long long)c0 + (long long)max(w, 0) * per, (long long)c1);
       const int e1 = (int)min((long long)e0 + per, (long long)c1);
       Cut c;
-      bool cut = w < GP && e0 < e1;
+      bool cut = w < kA8Warps && e0 < e1;
       if (cut) {
-        locate(w < 0 ? c0 : e1 - 1, c.b, c.h, c.s0, c.s1);
+        int tile;
+        locate(w < 0 ? c0 : e1 - 1, c.b, c.h, tile, c.s0, c.s1);
         cut = w < 0 ? c.s0 < c0 : c.s0 >= e0 && c.s1 > e1;
         c.first = max(w, 0);
-        c.last = min(GP - 1, (min(c.s1, c1) - 1 - c0) / per);
-        c.rows = min(max(s_row[c.b + 1] - s_row[c.b], 0), a.max_q) * G;
+        c.last = min(kA8Warps - 1, (min(c.s1, c1) - 1 - c0) / per);
+        c.row0 = tile * kA8Rows;
+        c.rows = min(kA8Rows, min(max(s_row[c.b + 1] - s_row[c.b], 0), a.max_q) * G - c.row0);
         c.from_tail = w >= 0;
       }
       const unsigned mask = __ballot_sync(0xffffffffu, cut);
@@ -639,9 +640,6 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     }
   };
 
-  // The ring is filled `lag` pages behind the one just read (other warps of
-  // the worker may still read that one).
-  const int lag = NT == 1 ? 0 : 1;
   if (n_units > 0) begin_segment(g0);
   {
     lookup(lane, bl0, lg0);
@@ -649,11 +647,9 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     found(lane, bl0, lg0);
     if (n_units > 32) found(32 + lane, bl1, lg1);
   }
-  if (wt == 0) {
-    #pragma unroll 1
-    for (int i = 0; i < min(S - lag, n_units); ++i) issue(i);
-  }
-  take_queries();
+  #pragma unroll 1
+  for (int i = 0; i < min(kA8Ring, n_units); ++i) issue(i);
+  if (n_units > 0) take_queries();
   find_cuts();
   #pragma unroll 1
   for (int k = 0;; ++k) {
@@ -662,9 +658,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
         const bool head = my_seg->begin < g0;
         float* dst = head ? my_head : nullptr;
         if (k == n_units && !head && seg_end > g1) {
-          // the tail goes into the worker's own ring, which is idle now
-          if (NT > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + worker), "r"(32 * NT) : "memory");
-          dst = reinterpret_cast<float*>(my_ring);
+          dst = reinterpret_cast<float*>(my_ring);       // the tail: the ring is idle now
         }
         flush(dst);
       }
@@ -678,42 +672,33 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
       lg0 = lg1;
       lookup(k + 32 + lane, bl1, lg1);
     }
-    if ((k & 31) == 16 && k > 16) found(k + 16 + lane, bl1, lg1);      // the ring is at most 16 pages ahead
-    const int lp = __shfl_sync(0xffffffffu, lg0, k & 31), stage = k & (S - 1);
+    if ((k & 31) == 16 && k > 16) found(k + 16 + lane, bl1, lg1);      // the loads are back
+    const int lp = __shfl_sync(0xffffffffu, lg0, k & 31), stage = k & (kA8Ring - 1);
     if (gave_up < 0) {
-      const bool ok = mbar_wait(full0 + 8 * stage, (k >> s_log2) & 1);
-      if (!__all_sync(0xffffffffu, ok)) gave_up = min(n_units, k + S - lag);
+      const bool ok = mbar_wait(full0 + 8 * stage, (k / kA8Ring) & 1);
+      if (!__all_sync(0xffffffffu, ok)) gave_up = min(n_units, k + kA8Ring);
     }
-    if (live && gave_up < 0 && lp >= 0) process(my_ring + stage * BLK, lp);
+    if (gave_up < 0 && lp >= 0) process(my_ring + stage * BLK, lp);
     __syncwarp();
-    if (NT > 1 && lane == 0) mbar_arrive(empty0 + 8 * stage);
-    const int next = k + S - lag;
-    if (wt == 0 && next < n_units && gave_up < 0) {
-      if (NT > 1 && next >= S) {
-        const bool ok = mbar_wait(empty0 + 8 * (next & (S - 1)), ((next >> s_log2) - 1) & 1);
-        if (!__all_sync(0xffffffffu, ok)) gave_up = next;
-      }
-      if (gave_up < 0) issue(next);
-    }
+    if (k + kA8Ring < n_units && gave_up < 0) issue(k + kA8Ring);
   }
   if (gave_up >= 0) {
     if (lane == 0) atomicOr(ga.status, 1u);
     // copies still in flight land before the ring is used again
-    if (wt == 0)
-      for (int i = max(0, gave_up - S); i < gave_up; ++i) mbar_wait(full0 + 8 * (i & (S - 1)), (i >> s_log2) & 1);
+    for (int i = max(0, gave_up - kA8Ring); i < gave_up; ++i) mbar_wait(full0 + 8 * (i & (kA8Ring - 1)), (i / kA8Ring) & 1);
   }
   __syncthreads();
 
   // ---- merge the pieces of cut segments
   constexpr int D4 = HD / 4;
-  const int per_seg = ga.rows * D4;
+  const int tile_rows = min(kA8Rows, G * a.max_q), per_seg = tile_rows * D4;
   for (int e = tid; e < s_ncut * per_seg; e += kA8Threads) {
     const Cut& c = s_cut[e / per_seg];
     const int row = e % per_seg / D4, d = e % D4 * 4;
     if (row >= c.rows) continue;
     auto piece = [&](int x) {
-      return (c.from_tail && x == c.first ? reinterpret_cast<const float*>(ring + (size_t)x * S * BLK)
-                                          : heads + (size_t)x * NT * ROWS * SROW) + (size_t)row * SROW;
+      return (c.from_tail && x == c.first ? reinterpret_cast<const float*>(ring + x * kA8Ring * BLK)
+                                          : heads + x * kA8Rows * SROW) + row * SROW;
     };
     float M = kNoMax, MO = kNoMax, L = 0.f;
     #pragma unroll 4
@@ -733,12 +718,12 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
       acc.x += f * y.x; acc.y += f * y.y; acc.z += f * y.z; acc.w += f * y.w;
     }
     if (c.s0 >= c0 && c.s1 <= c1) {
-      const int src = s_row[c.b] + row / G;
+      const int of_seq = c.row0 + row, src = s_row[c.b] + of_seq / G;
       const float f = final_factor(M, L, MO);
       if (src >= 0 && src < a.n_q)
-        put(src, c.h * G + row % G, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+        put(src, c.h * G + of_seq % G, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
     } else {
-      float* dst = ga.part + (((size_t)blockIdx.x * 2 + (c.s0 < c0 ? 0 : 1)) * ga.rows + row) * SROW;
+      float* dst = ga.part + ((blockIdx.x * 2 + (c.s0 < c0 ? 0 : 1)) * kA8Rows + row) * SROW;
       *reinterpret_cast<float4*>(dst + d) = acc;
       if (d == 0) *reinterpret_cast<float4*>(dst + HD) = make_float4(M, L, MO, 0.f);
     }
@@ -761,7 +746,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   }
   __syncthreads();
   float* s_fac = reinterpret_cast<float*>(ring);        // [rows][partials]
-  float* s_out = s_fac + ga.rows * kA8MaxCtas;          // [rows]
+  float* s_out = s_fac + kA8Rows * kA8MaxCtas;          // [rows]
   #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if (!s_last[i]) continue;
@@ -769,7 +754,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     const int first = c.s0 / per_cta, n_c = (c.s1 - 1) / per_cta - first + 1;
     // partial of the x-th CTA: the segment begins in the first one
     auto piece = [&](int x, int row) {
-      return ga.part + (((size_t)(first + x) * 2 + (x == 0 ? 1 : 0)) * ga.rows + row) * SROW;
+      return ga.part + (((first + x) * 2 + (x == 0 ? 1 : 0)) * kA8Rows + row) * SROW;
     };
     __syncthreads();                                    // s_fac of the other segment is read
     for (int row = warp; row < c.rows; row += kA8Warps) {
@@ -806,10 +791,10 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
         const float f = s_fac[row * kA8MaxCtas + x];
         acc.x += f * y.x; acc.y += f * y.y; acc.z += f * y.z; acc.w += f * y.w;
       }
-      const int src = s_row[c.b] + row / G;
+      const int of_seq = c.row0 + row, src = s_row[c.b] + of_seq / G;
       const float f = s_out[row];
       if (src >= 0 && src < a.n_q)
-        put(src, c.h * G + row % G, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+        put(src, c.h * G + of_seq % G, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
     }
   }
 }
@@ -832,7 +817,7 @@ static_assert(kA8TicketsAt + 4 * kA8MaxCtas <= kA8PartAt, "tickets overlap the p
 template <int HD, int TYPE, bool SPLIT, bool MODS>
 static cudaError_t attn8_launch(const Attn8Args& g, int grid, cudaStream_t st) {
   auto kern = k_kv8_attn<HD, TYPE, SPLIT, MODS>;
-  const size_t fixed = (size_t)kA8Stages * kv8_block_bytes(HD) + 4ull * kA8Warps * 8 * (HD + 4) + 16ull * kA8Stages;
+  const size_t fixed = kA8Warps * (kA8Ring * (kv8_block_bytes(HD) + 8ull) + 4ull * kA8Rows * (HD + 4));
   // once per device: the most that any batch needs
   static std::atomic<unsigned long long> ready{0};
   int dev = 0;
@@ -849,7 +834,7 @@ static cudaError_t attn8_launch(const Attn8Args& g, int grid, cudaStream_t st) {
 
 extern "C" size_t bc_kv8_attention_scratch_bytes(int batch, int n_kv_heads, int group, int max_q, int head_dim) {
   if (!attn8_sizes_ok(batch, n_kv_heads, group, max_q, head_dim)) return 0;
-  return kA8PartAt + 4ull * kA8MaxCtas * 2 * group * max_q * (head_dim + 4);
+  return kA8PartAt + 4ull * kA8MaxCtas * 2 * kA8Rows * (head_dim + 4);
 }
 
 extern "C" bc_status bc_kv8_attention(const bc_kv8_attention_args* a, void* stream) {
@@ -869,8 +854,9 @@ extern "C" bc_status bc_kv8_attention(const bc_kv8_attention_args* a, void* stre
     return entry_fail(BC_EINVAL, "%s: bad page or row counts", who);
   if ((long long)a->n_pages * a->n_kv_heads > INT32_MAX)
     return entry_fail(BC_EINVAL, "%s: more than 2^31 - 1 blocks in the pool", who);
-  if ((long long)a->batch * a->n_kv_heads * std::max(a->max_blocks, a->pages ? a->max_sel : 0) > INT32_MAX)
-    return entry_fail(BC_EINVAL, "%s: more than 2^31 - 1 pages over all sequences and heads", who);
+  const int tiles = (a->group * a->max_q + kA8Rows - 1) / kA8Rows;
+  if ((long long)a->batch * a->n_kv_heads * std::max(a->max_blocks, a->pages ? a->max_sel : 0) > INT32_MAX / tiles)
+    return entry_fail(BC_EINVAL, "%s: too many pages over all sequences, heads and rows", who);
   if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->pool, 16))
     return entry_fail(BC_EINVAL, "%s: q, out and pool must be 16-byte aligned", who);
   if (a->q_stride % 8 || a->q_stride < (long long)a->n_kv_heads * a->group * a->head_dim)
@@ -886,10 +872,6 @@ extern "C" bc_status bc_kv8_attention(const bc_kv8_attention_args* a, void* stre
   g.a = *a;
   // a window that reaches every token is none
   if (a->window >= (long long)a->max_blocks * kPage + 64) g.a.window = 0;
-  g.rows = a->group * a->max_q;
-  g.nt_log2 = 0;
-  while ((8 << g.nt_log2) < g.rows) ++g.nt_log2;
-  g.nt = 1 << g.nt_log2;
   char* sc = static_cast<char*>(a->scratch);
   g.status = reinterpret_cast<unsigned*>(sc);
   g.tickets = reinterpret_cast<unsigned*>(sc + kA8TicketsAt);

@@ -529,9 +529,9 @@ BC_API bc_status bc_kv8_gather(const void* pool, bc_kv8_type type, int n_pages, 
  *            first call (every call leaves the tickets at zero).  Calls of any
  *            sizes can share it, calls that may overlap on the GPU not.
  * Lengths outside [0, 16 max_blocks] are taken as the nearest bound.
- * max_blocks <= 2^25, n_q <= 2^29, and n_pages * n_kv_heads and batch *
- * n_kv_heads * (the larger of max_blocks and, with pages, max_sel) are at most
- * 2^31 - 1.
+ * max_blocks <= 2^25, n_q <= 2^29, and n_pages * n_kv_heads and ceil(group *
+ * max_q / 8) * batch * n_kv_heads * (the larger of max_blocks and, with pages,
+ * max_sel) are at most 2^31 - 1.
  * Deterministic for the same sizes and lengths.
  * Errors: BC_EINVAL, BC_ENOMEM, BC_ECUDA. */
 typedef struct {
