@@ -11,9 +11,10 @@
 // rows); the pages of all segments, in that order, are one line of units; it
 // is cut into equal pieces, one per warp, whatever the lengths are: a warp's
 // piece may begin and end inside a segment and hold several.  A CTA (one per
-// SM) has 16 warps.  A warp reads its pages through a ring in shared memory,
+// SM) has 12 warps.  A warp reads its pages through a ring in shared memory,
 // filled by bulk copies (a block of a page and head, scales included, is
-// contiguous) 2 pages ahead, 32 blocks per SM; the page numbers come from
+// contiguous) 2 pages ahead, 24 blocks per SM (32 only lengthen the
+// queues: 84 against 80 us for 64 sequences of 1K to 8K tokens); the page numbers come from
 // registers, 64 units ahead.  Sequences with more than 8 rows (several
 // queries, or drafts) have their blocks read once per 8 rows, mostly from L2;
 // the products, not the bytes, bound those (sharing a block between the warps
@@ -57,7 +58,7 @@
 
 namespace bc {
 
-constexpr int kA8Warps = 16, kA8Threads = kA8Warps * 32;
+constexpr int kA8Warps = 12, kA8Threads = kA8Warps * 32;
 constexpr int kA8Ring = 2;          // blocks in flight per warp
 constexpr int kA8Rows = 8;          // query rows per segment
 constexpr int kA8MaxCtas = 160;     // CTAs the scratch provides for

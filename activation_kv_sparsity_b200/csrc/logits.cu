@@ -4,12 +4,12 @@
 // Persistent CTAs take pieces of 2048 to 8192 ids, neighbours of a row one
 // after the other, and load a piece's logits (4 a thread and round) while the
 // one before is worked on.  A row's history and biases are read once per row
-// and CTA into shared memory.  For each piece, and for the history and the
-// biases in turn, the CTA walks the list and marks the ids that fall into the
-// piece, a word per id; each thread then looks its own ids up and clears their
-// words.  A word of the history is bit 31, "seen in the prompt", and the count
-// of the output tokens; a word of the biases the place of the last entry for
-// the id (a maximum), so no result depends on the order of the atomics.
+// and CTA into shared memory.  For each piece the CTA walks them and marks the
+// ids that fall into the piece, a word per id and list; each thread then looks
+// its own ids up and clears their words.  A word of the history is bit 31,
+// "seen in the prompt", and the count of the output tokens; a word of the
+// biases the place of the last entry for the id (a maximum), so no result
+// depends on the order of the atomics.
 // 160 rows of 128256 f32 logits with histories of up to 8192 tokens, 32 biases
 // and masks take 46 us (3.5 TB/s of logits; 29 us without lists, the copy's
 // rate); 68 us with a CTA a piece that walks the lists in L2, 55 us as a copy
@@ -77,7 +77,8 @@ __device__ __forceinline__ const uint32_t* mask_of(const bc_logits_args& a, int 
 template <typename T>
 __global__ void __launch_bounds__(kLogitThreads, kLogitCtas) k_logits(const __grid_constant__ LogitsArgs g) {
   extern __shared__ __align__(16) unsigned s_mark[];            // [kLogitRounds * kLogitRound]
-  int* s_list = reinterpret_cast<int*>(s_mark + kLogitRounds * kLogitRound);
+  unsigned* s_bias = s_mark + kLogitRounds * kLogitRound;       // the same for the biases
+  int* s_list = reinterpret_cast<int*>(s_bias + kLogitRounds * kLogitRound);
   // [kLogitList]: history, then biases, each padded to a multiple of 4
   const bc_logits_args& a = g.a;
   const int piece = g.rounds * kLogitRound;
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas) k_logits(const __gr
   float x[kLogitRounds][4], next[kLogitRounds][4];
   load(x, row, v0);
   #pragma unroll
-  for (int k = 0; k < kLogitRounds; ++k)
+  for (int k = 0; k < 2 * kLogitRounds; ++k)
     *reinterpret_cast<uint4*>(s_mark + k * kLogitRound + 4 * threadIdx.x) = make_uint4(0, 0, 0, 0);
 
   int at_row = -1, h0 = 0, h1 = 0, b0 = 0, b1 = 0, nh = 0, nb = 0;   // nh, nb: entries in shared memory
@@ -178,24 +179,6 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas) k_logits(const __gr
         for (int j = 0; j < kLogitWalk; j += 4) mark(i0 + j * kLogitThreads, v + j, (unsigned)kLogitThreads);
       }
     };
-    // apply(value, word) to the thread's marked ids, whose words are cleared
-    auto look_up = [&](auto apply) {
-      __syncthreads();
-      #pragma unroll
-      for (int k = 0; k < kLogitRounds; ++k) {
-        const int i = k * kLogitRound + 4 * threadIdx.x;
-        if (i >= n) break;
-        uint4* w = reinterpret_cast<uint4*>(s_mark + i);
-        const uint4 c = *w;
-        if (!(c.x | c.y | c.z | c.w)) continue;
-        *w = make_uint4(0, 0, 0, 0);
-        if (c.x) x[k][0] = apply(x[k][0], c.x);
-        if (c.y) x[k][1] = apply(x[k][1], c.y);
-        if (c.z) x[k][2] = apply(x[k][2], c.z);
-        if (c.w) x[k][3] = apply(x[k][3], c.w);
-      }
-      __syncthreads();
-    };
     if (h1 > h0) {
       walk(a.hist, h0, h1, 0, nh, [&](unsigned i, const unsigned* v, unsigned step) {
         if (i >= out0) {
@@ -210,19 +193,43 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas) k_logits(const __gr
           }
         }
       });
-      look_up([&](float y, unsigned c) {
-        y *= y > 0.f ? inv_rep : rep;
-        if (c & 0x7fffffffu) y -= __fmul_rn(freq, (float)(c & 0x7fffffffu)) + pres;
-        return y;
-      });
     }
     if (b1 > b0) {
       walk(a.bias_ids, b0, b1, (nh + 3) & ~3, nb,
            [&](unsigned i, const unsigned* v, unsigned step) {
              #pragma unroll
-             for (int j = 0; j < 4; ++j) max_if(s_mark + v[j], i + j * step - b0 + 1, v[j] < (unsigned)n);
+             for (int j = 0; j < 4; ++j) max_if(s_bias + v[j], i + j * step - b0 + 1, v[j] < (unsigned)n);
            });
-      look_up([&](float y, unsigned c) { return y + a.bias_vals[b0 + c - 1]; });
+    }
+    if (h1 > h0 || b1 > b0) {
+      __syncthreads();
+      // the thread's marked ids, whose words are cleared
+      #pragma unroll
+      for (int k = 0; k < kLogitRounds; ++k) {
+        const int i = k * kLogitRound + 4 * threadIdx.x;
+        if (i >= n) break;
+        const uint4 c4 = *reinterpret_cast<const uint4*>(s_mark + i);
+        if (c4.x | c4.y | c4.z | c4.w) {
+          *reinterpret_cast<uint4*>(s_mark + i) = make_uint4(0, 0, 0, 0);
+          const unsigned c[4] = {c4.x, c4.y, c4.z, c4.w};
+          #pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (!c[j]) continue;
+            x[k][j] *= x[k][j] > 0.f ? inv_rep : rep;
+            if (c[j] & 0x7fffffffu) x[k][j] -= __fmul_rn(freq, (float)(c[j] & 0x7fffffffu)) + pres;
+          }
+        }
+        if (b1 == b0) continue;
+        const uint4 w4 = *reinterpret_cast<const uint4*>(s_bias + i);
+        if (w4.x | w4.y | w4.z | w4.w) {
+          *reinterpret_cast<uint4*>(s_bias + i) = make_uint4(0, 0, 0, 0);
+          const unsigned w[4] = {w4.x, w4.y, w4.z, w4.w};
+          #pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (w[j]) x[k][j] += a.bias_vals[b0 + w[j] - 1];
+        }
+      }
+      __syncthreads();
     }
     T* dst = static_cast<T*>(a.out) + (long long)row * a.out_stride + v0;
     const bool wide = (reinterpret_cast<uintptr_t>(dst) & (4 * sizeof(T) - 1)) == 0;
@@ -257,7 +264,7 @@ using namespace bc;
 
 template <typename T>
 static cudaError_t launch_logits(const LogitsArgs& g, dim3 grid, cudaStream_t st) {
-  constexpr int smem = 4 * (kLogitRounds * kLogitRound + kLogitList);
+  constexpr int smem = 4 * (2 * kLogitRounds * kLogitRound + kLogitList);
   static std::atomic<unsigned long long> ready{0};     // once per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
