@@ -55,6 +55,7 @@
 #include "entry.h"
 #include "kv8.cuh"
 
+#include <math.h>
 #include <algorithm>
 #include <atomic>
 
@@ -192,8 +193,10 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const uint32_t full0 = smem_addr(bars) + 8 * warp * kA8Ring;
-  if (tid < kA8Warps * kA8Ring) mbar_init(smem_addr(bars) + 8 * tid, 1);
-  if (tid == 0) mbar_init_fence();
+  if (tid < kA8Warps * kA8Ring) {
+    mbar_init(smem_addr(bars) + 8 * tid, 1);
+    mbar_init_fence();
+  }
   pdl_wait();
   pdl_trigger();
 
@@ -528,6 +531,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
         uint4* x = reinterpret_cast<uint4*>(blk + kPage * HD + (8 * v + g) * 64 + t * 16);
         *x = make_uint4(x->x & keep, x->y & keep, x->z & keep, x->w & keep);
       }
+      // these stores come before the next copy into this block
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     uint32_t ph[2], pl[2];
     #pragma unroll
@@ -865,8 +870,8 @@ extern "C" bc_status bc_kv8_attention(const bc_kv8_attention_args* a, void* stre
   if (a->q_stride % 8 || a->q_stride < (long long)a->n_kv_heads * a->group * a->head_dim)
     return entry_fail(BC_EINVAL, "%s: q_stride must be a multiple of 8 and cover the heads", who);
   if (!aligned(a->scratch, 256)) return entry_fail(BC_EINVAL, "%s: scratch must be 256-byte aligned", who);
-  if (!(a->cap >= 0.f) || a->window < 0 || !(a->scale == a->scale))
-    return entry_fail(BC_EINVAL, "%s: cap and window must not be negative, scale a number", who);
+  if (!(a->cap >= 0.f && a->cap <= 3.4e38f) || a->window < 0 || !(fabsf(a->scale) <= 3.4e38f))
+    return entry_fail(BC_EINVAL, "%s: cap and window must not be negative, cap and scale finite", who);
   if (a->scratch_bytes < bc_kv8_attention_scratch_bytes(a->batch, a->n_kv_heads, a->group, a->max_q, a->head_dim))
     return entry_fail(BC_ENOMEM, "%s: scratch too small", who);
   if (a->n_q == 0) return BC_OK;
