@@ -753,57 +753,70 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     s_last[tid] = last;
   }
   __syncthreads();
-  float* s_fac = reinterpret_cast<float*>(ring);        // [rows][partials]
-  float* s_out = s_fac + kA8Rows * kA8MaxCtas;          // [rows]
-  #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  if (!s_last[0] && !s_last[1]) return;
+  float* s_fac = reinterpret_cast<float*>(ring);        // [2][kA8Rows][partials]
+  float* s_out = s_fac + 2 * kA8Rows * kA8MaxCtas;      // [2][kA8Rows]
+  // partial of row `row` in the x-th CTA of segment c, which begins in the first one
+  auto first_of = [&](const Cut& c) { return c.s0 / per_cta; };
+  auto count_of = [&](const Cut& c) { return (c.s1 - 1) / per_cta - c.s0 / per_cta + 1; };
+  auto partial = [&](const Cut& c, int x, int row) {
+    return ga.part + (((first_of(c) + x) * 2 + (x == 0 ? 1 : 0)) * kA8Rows + row) * SROW;
+  };
+  // both slots at once: a warp a row for the weights, then a thread 4 dims
+  for (int ir = warp; ir < 2 * kA8Rows; ir += kA8Warps) {
+    const int i = ir / kA8Rows, row = ir % kA8Rows;
     if (!s_last[i]) continue;
     const Cut& c = s_cut[s_out_cut[i]];
-    const int first = c.s0 / per_cta, n_c = (c.s1 - 1) / per_cta - first + 1;
-    // partial of the x-th CTA: the segment begins in the first one
-    auto piece = [&](int x, int row) {
-      return ga.part + (((first + x) * 2 + (x == 0 ? 1 : 0)) * kA8Rows + row) * SROW;
-    };
-    __syncthreads();                                    // s_fac of the other segment is read
-    for (int row = warp; row < c.rows; row += kA8Warps) {
-      float M = kNoMax, MO = kNoMax, L = 0.f;
-      float4 ml[kA8MaxCtas / 32];
-      #pragma unroll
-      for (int j = 0; j < kA8MaxCtas / 32; ++j) {
-        ml[j] = make_float4(kNoMax, 0.f, kNoMax, 0.f);
-        if (32 * j + lane < n_c) ml[j] = __ldcg(reinterpret_cast<const float4*>(piece(32 * j + lane, row) + HD));
-        M = fmaxf(M, ml[j].x);
-        MO = fmaxf(MO, ml[j].z);
-      }
-      #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, o));
-      }
-      #pragma unroll
-      for (int j = 0; j < kA8MaxCtas / 32; ++j) {
-        L += ex2(ml[j].x - M) * ml[j].y;
-        if (32 * j + lane < n_c) s_fac[row * kA8MaxCtas + 32 * j + lane] = ex2(ml[j].z - MO);
-      }
-      #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-      if (lane == 0) s_out[row] = final_factor(M, L, MO);
+    if (row >= c.rows) continue;
+    const int n_c = count_of(c);
+    float M = kNoMax, MO = kNoMax, L = 0.f;
+    float4 ml[kA8MaxCtas / 32];
+    #pragma unroll
+    for (int j = 0; j < kA8MaxCtas / 32; ++j) {
+      ml[j] = make_float4(kNoMax, 0.f, kNoMax, 0.f);
+      if (32 * j + lane < n_c) ml[j] = __ldcg(reinterpret_cast<const float4*>(partial(c, 32 * j + lane, row) + HD));
+      M = fmaxf(M, ml[j].x);
+      MO = fmaxf(MO, ml[j].z);
     }
-    __syncthreads();
-    for (int e = tid; e < c.rows * D4; e += kA8Threads) {
-      const int row = e / D4, d = e % D4 * 4;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      #pragma unroll 8
-      for (int x = 0; x < n_c; ++x) {
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(piece(x, row) + d));
-        const float f = s_fac[row * kA8MaxCtas + x];
-        acc.x += f * y.x; acc.y += f * y.y; acc.z += f * y.z; acc.w += f * y.w;
-      }
-      const int of_seq = c.row0 + row, src = s_row[c.b] + of_seq / G;
-      const float f = s_out[row];
-      if (src >= 0 && src < a.n_q)
-        put(src, c.h * G + of_seq % G, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+    #pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, o));
     }
+    #pragma unroll
+    for (int j = 0; j < kA8MaxCtas / 32; ++j) {
+      L += ex2(ml[j].x - M) * ml[j].y;
+      if (32 * j + lane < n_c) s_fac[ir * kA8MaxCtas + 32 * j + lane] = ex2(ml[j].z - MO);
+    }
+    #pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane == 0) s_out[ir] = final_factor(M, L, MO);
+  }
+  __syncthreads();
+  for (int e = tid; e < 2 * per_seg; e += kA8Threads) {
+    const int i = e >= per_seg, row = (e - i * per_seg) / D4, d = e % D4 * 4;
+    if (!s_last[i]) continue;
+    const Cut& c = s_cut[s_out_cut[i]];
+    if (row >= c.rows) continue;
+    const int n_c = count_of(c), ir = i * kA8Rows + row;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x0 = 0; x0 < n_c; x0 += 8) {               // 8 partials in flight, the last ones too
+      float4 y[8];
+      #pragma unroll
+      for (int j = 0; j < 8; ++j)
+        y[j] = x0 + j < n_c ? __ldcg(reinterpret_cast<const float4*>(partial(c, x0 + j, row) + d))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+      #pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (x0 + j >= n_c) break;
+        const float f = s_fac[ir * kA8MaxCtas + x0 + j];
+        acc.x += f * y[j].x; acc.y += f * y[j].y; acc.z += f * y[j].z; acc.w += f * y[j].w;
+      }
+    }
+    const int of_seq = c.row0 + row, src = s_row[c.b] + of_seq / G;
+    const float f = s_out[ir];
+    if (src >= 0 && src < a.n_q)
+      put(src, c.h * G + of_seq % G, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
   }
 }
 

@@ -438,7 +438,7 @@ def run_logits(B, V, dtype, seed, hist=None, bias=0, masks=0, rows=False, pads=F
     big = np.abs(x.double().numpy()) * 2 + (1.5 * ((hist or 0) + 1)) + 25.0
     tol = 5 * 2.0 ** -24 * big + (np.abs(want) * 2.0 ** -8 if dtype == torch.bfloat16 else 0.0)
     ok = np.isfinite(want)
-    assert (np.abs(got - want)[ok] <= tol[ok]).all()
+    assert (np.abs(got[ok] - want[ok]) <= tol[ok]).all()
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
