@@ -714,3 +714,61 @@ def test_wrappers_say_what_is_wrong():
     for k, v in dict(lens=i(3), q_start=i(2), positions=i(3), n_free=i(2), delta=i(2).float(), free_list=i(10)[::2]).items():
         refused(k, bc.block_tables, **{**t, k: v})
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ beyond 32 bits
+def test_a_pool_beyond_4_gib():
+    """Pages whose bytes lie past 2^32 in the pool: the same bits as from a
+    small pool."""
+    H, G, hd, code = 8, 4, 128, "e4m3"
+    block = og.block_bytes(hd)
+    n_pages = 2 ** 32 // (H * block) + 40
+    big = torch.empty(n_pages, H, block, dtype=torch.uint8, device=DEV)
+    small = torch.zeros(12, H, block, dtype=torch.uint8, device=DEV)
+    shift = n_pages - 12
+    assert shift * H * block > 2 ** 32
+    g = gen(5)
+    n = 12 * 16 - 3
+    k, v = (torch.randn(n, H, hd, generator=g).to(DEV) for _ in range(2))
+    q = torch.randn(1, H * G, hd, generator=g).to(DEV)
+    res = []
+    for pool, first in ((small, 0), (big, shift)):
+        pages = torch.arange(first, first + 12, device=DEV).flip(0).int()
+        pos = torch.arange(n, device=DEV)
+        slots = (pages[pos // 16] * 16 + pos % 16).int()
+        bc.kv8_append(k, v, slots, pool, code)
+        ko, vo = torch.empty_like(k), torch.empty_like(v)
+        bc.kv8_gather(pool, slots, ko, vo, code)
+        out = torch.empty_like(q)
+        scratch = torch.zeros(bc.bc_kv8_attention_scratch_bytes(1, H, G, 1, hd), dtype=torch.uint8, device=DEV)
+        bc.kv8_attention(q, pool, ints([n]), pages[None].contiguous(), out, scratch, code)
+        res.append((ko, vo, out))
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+    assert (res[0][0] - k).abs().max() < 0.07 * k.abs().max()
+
+
+def test_outputs_beyond_2_31_elements():
+    H, hd, n = 8, 128, 2 ** 31 // (8 * 128) + 50
+    pool = to(DEV, make_pool(3, H, hd, "int8", seed=6))
+    slots = (torch.arange(n, device=DEV) * 7 % 48).int()
+    k = torch.empty(n, H, hd, dtype=torch.bfloat16, device=DEV)
+    v = torch.empty_like(k)
+    bc.kv8_gather(pool, slots, k, v, "int8")
+    rk, rv = og.read(pool.cpu().numpy(), slots[-60:].cpu().numpy(), "int8", hd)
+    assert torch.equal(k[-60:].cpu(), torch.from_numpy(rk).float().to(torch.bfloat16))
+    assert torch.equal(v[-60:].cpu(), torch.from_numpy(rv).float().to(torch.bfloat16))
+    del k, v
+    B, V = 17000, 128256
+    assert B * V > 2 ** 31
+    x = torch.zeros(B, V, dtype=torch.bfloat16, device=DEV)
+    x[-1] = 2.0
+    hist = ints([5, V - 1, 5])
+    starts = torch.zeros(B + 1, dtype=torch.int32, device=DEV)
+    starts[-1] = 3
+    bc.logits_adjust(x, x, hist=hist, hist_start=starts, repetition=torch.full((B,), 2.0, device=DEV),
+                     frequency=torch.full((B,), 0.25, device=DEV))
+    assert (x[:-1] == 0).all()
+    want = torch.full((V,), 2.0)
+    want[5], want[V - 1] = 0.5, 0.75
+    assert torch.equal(x[-1].float().cpu(), want)
