@@ -74,6 +74,16 @@ struct Attn8Args {
   unsigned* status;       // bit 0: a wait gave up
 };
 
+// x / d for x < 2^31 and a quotient below 2^20: the float quotient is off by
+// less than 1
+__device__ __forceinline__ unsigned small_div(unsigned x, unsigned d) {
+  unsigned q = (unsigned)__fdividef((float)x, (float)d);
+  const int rest = (int)(x - q * d);
+  if (rest < 0) --q;
+  else if (rest >= (int)d) ++q;
+  return q;
+}
+
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -256,22 +266,24 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   const int g0 = (int)min((long long)c0 + (long long)warp * per, (long long)c1);
   const int g1 = (int)min((long long)g0 + per, (long long)c1);
 
+  // row / G for the rows of a kv head (G <= 8, rows < 72): one multiplication
+  const int g_inv = 65536 / G + 1;
+  auto query_of = [&](int row) { return row * g_inv >> 16; };
   auto seq_at = [&](int b) { return seq_of(a, s_len[b], s_row[b], s_row[b + 1] - s_row[b], b); };
   // the segment of unit u: sequence, kv head, 8 rows, units
   auto locate = [&](int u, int& b, int& h, int& tile, int& begin, int& end) {
-    const int x = (unsigned)u / (unsigned)H;
-    int lo = 0, hi = B;                      // last b with s_cum[b] <= x
+    int lo = 0, hi = B;                      // last b with s_cum[b] H <= u
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (s_cum[mid] <= x) lo = mid;
+      if (s_cum[mid] * H <= u) lo = mid;
       else hi = mid;
     }
     b = lo;
     const int tiles = (min(max(s_row[b + 1] - s_row[b], 0), a.max_q) * G + kA8Rows - 1) / kA8Rows;
     const unsigned of_head = s_cum[b + 1] - s_cum[b], at = u - s_cum[b] * H;
     const unsigned cnt = tiles == 1 ? of_head : of_head / (unsigned)tiles;
-    h = at / of_head;
-    tile = tiles == 1 ? 0 : (at - h * of_head) / cnt;
+    h = small_div(at, of_head);
+    tile = tiles == 1 ? 0 : small_div(at - h * of_head, cnt);
     begin = s_cum[b] * H + h * of_head + tile * cnt;
     end = begin + cnt;
   };
@@ -362,17 +374,17 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
       const int row = row0 + 2 * t + i;
       at[i] = INT32_MAX;
       if (row < s.rows) {
-        at[i] = first + row / G;
+        at[i] = first + query_of(row);
         if (a.window > 0) w_lo = max(w_lo, at[i] - a.window + 1);
         w_hi = min(w_hi, at[i]);
       }
-      slope[i] = MODS && a.slopes && row < s.rows ? a.slopes[h * G + row % G] : 0.f;
+      slope[i] = MODS && a.slopes && row < s.rows ? a.slopes[h * G + row - query_of(row) * G] : 0.f;
     }
     all_lo = __reduce_max_sync(0xffffffffu, w_lo);
     all_hi = __reduce_min_sync(0xffffffffu, w_hi);
-    const int row = row0 + g, src = s.r0 + row / G;
+    const int row = row0 + g, query = query_of(row), src = s.r0 + query;
     const bool ok = row < s.rows && src >= 0 && src < a.n_q;
-    const size_t e0 = (size_t)(ok ? src : 0) * a.q_stride + (size_t)(ok ? h * G + row % G : 0) * HD + 16 * t;
+    const size_t e0 = (size_t)(ok ? src : 0) * a.q_stride + (size_t)(ok ? (h - query) * G + row : 0) * HD + 16 * t;
     #pragma unroll
     for (int i = 0; i < NRAW; ++i) {
       const size_t e = e0 + (SPLIT ? 64 * (i / 4) + 4 * (i % 4) : 64 * (i / 2) + 8 * (i % 2));
@@ -585,14 +597,14 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
       if (gave_up >= 0) ll = __uint_as_float(0x7fc00000u);
       const int in = 2 * t + i, row = s.row0 + in;
       const float f = final_factor(m[i], ll, mo[i]);
-      const int src = s.r0 + row / G;
+      const int query = query_of(row), src = s.r0 + query;
       const bool ok = row < s.rows && src >= 0 && src < a.n_q;
       #pragma unroll
       for (int v = 0; v < V4; ++v) {
         const float4 y = make_float4(o[v][0][i], o[v][0][2 + i], o[v][1][i], o[v][1][2 + i]);
         const int d = 4 * (8 * v + g);
         if (dst) *reinterpret_cast<float4*>(dst + in * SROW + d) = y;
-        else if (ok) put(src, s.h * G + row % G, d, make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
+        else if (ok) put(src, (s.h - query) * G + row, d, make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
       }
       if (dst && g == 0) {
         float* ml = dst + in * SROW + HD;
@@ -612,6 +624,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   // while the first pages are on their way.
   struct Cut {
     int b, h, s0, s1, first, last;   // segment, its units, the warps that hold pieces
+    int cta0, cta1;                  // the CTAs it begins and ends in
     int row0, rows;                  // its first row, and how many
     bool from_tail;
   };
@@ -629,7 +642,9 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
         locate(w < 0 ? c0 : e1 - 1, c.b, c.h, tile, c.s0, c.s1);
         cut = w < 0 ? c.s0 < c0 : c.s0 >= e0 && c.s1 > e1;
         c.first = max(w, 0);
-        c.last = min(kA8Warps - 1, (min(c.s1, c1) - 1 - c0) / per);
+        c.last = min(kA8Warps - 1, (int)small_div(min(c.s1, c1) - 1 - c0, per));
+        c.cta0 = small_div(c.s0, per_cta);
+        c.cta1 = small_div(c.s1 - 1, per_cta);
         c.row0 = tile * kA8Rows;
         c.rows = min(kA8Rows, min(max(s_row[c.b + 1] - s_row[c.b], 0), a.max_q) * G - c.row0);
         c.from_tail = w >= 0;
@@ -701,8 +716,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   constexpr int D4 = HD / 4;
   const int tile_rows = min(kA8Rows, G * a.max_q), per_seg = tile_rows * D4;
   for (int e = tid; e < s_ncut * per_seg; e += kA8Threads) {
-    const Cut& c = s_cut[e / per_seg];
-    const int row = e % per_seg / D4, d = e % D4 * 4;
+    const int which = small_div(e, per_seg), row = (e - which * per_seg) / D4, d = e % D4 * 4;
+    const Cut& c = s_cut[which];
     if (row >= c.rows) continue;
     auto piece = [&](int x) {
       return (c.from_tail && x == c.first ? reinterpret_cast<const float*>(ring + x * kA8Ring * BLK)
@@ -726,10 +741,10 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
       acc.x += f * y.x; acc.y += f * y.y; acc.z += f * y.z; acc.w += f * y.w;
     }
     if (c.s0 >= c0 && c.s1 <= c1) {
-      const int of_seq = c.row0 + row, src = s_row[c.b] + of_seq / G;
+      const int of_seq = c.row0 + row, query = query_of(of_seq), src = s_row[c.b] + query;
       const float f = final_factor(M, L, MO);
       if (src >= 0 && src < a.n_q)
-        put(src, c.h * G + of_seq % G, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+        put(src, (c.h - query) * G + of_seq, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
     } else {
       float* dst = ga.part + ((blockIdx.x * 2 + (c.s0 < c0 ? 0 : 1)) * kA8Rows + row) * SROW;
       *reinterpret_cast<float4*>(dst + d) = acc;
@@ -744,10 +759,10 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     bool last = false;
     if (s_nout >> tid & 1) {
       const Cut& c = s_cut[s_out_cut[tid]];
-      unsigned* ticket = ga.tickets + c.s0 / per_cta;
+      unsigned* ticket = ga.tickets + c.cta0;
       unsigned prev;
       asm volatile("atom.add.acq_rel.gpu.u32 %0, [%1], 1;" : "=r"(prev) : "l"(ticket) : "memory");
-      last = prev == (unsigned)((c.s1 - 1) / per_cta - c.s0 / per_cta);
+      last = prev == (unsigned)(c.cta1 - c.cta0);
       if (last) *ticket = 0u;
     }
     s_last[tid] = last;
@@ -757,10 +772,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   float* s_fac = reinterpret_cast<float*>(ring);        // [2][kA8Rows][partials]
   float* s_out = s_fac + 2 * kA8Rows * kA8MaxCtas;      // [2][kA8Rows]
   // partial of row `row` in the x-th CTA of segment c, which begins in the first one
-  auto first_of = [&](const Cut& c) { return c.s0 / per_cta; };
-  auto count_of = [&](const Cut& c) { return (c.s1 - 1) / per_cta - c.s0 / per_cta + 1; };
   auto partial = [&](const Cut& c, int x, int row) {
-    return ga.part + (((first_of(c) + x) * 2 + (x == 0 ? 1 : 0)) * kA8Rows + row) * SROW;
+    return ga.part + (((c.cta0 + x) * 2 + (x == 0 ? 1 : 0)) * kA8Rows + row) * SROW;
   };
   // both slots at once: a warp a row for the weights, then a thread 4 dims
   for (int ir = warp; ir < 2 * kA8Rows; ir += kA8Warps) {
@@ -768,7 +781,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     if (!s_last[i]) continue;
     const Cut& c = s_cut[s_out_cut[i]];
     if (row >= c.rows) continue;
-    const int n_c = count_of(c);
+    const int n_c = c.cta1 - c.cta0 + 1;
     float M = kNoMax, MO = kNoMax, L = 0.f;
     float4 ml[kA8MaxCtas / 32];
     #pragma unroll
@@ -798,7 +811,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     if (!s_last[i]) continue;
     const Cut& c = s_cut[s_out_cut[i]];
     if (row >= c.rows) continue;
-    const int n_c = count_of(c), ir = i * kA8Rows + row;
+    const int n_c = c.cta1 - c.cta0 + 1, ir = i * kA8Rows + row;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int x0 = 0; x0 < n_c; x0 += 8) {               // 8 partials in flight, the last ones too
       float4 y[8];
@@ -813,10 +826,10 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
         acc.x += f * y[j].x; acc.y += f * y[j].y; acc.z += f * y[j].z; acc.w += f * y[j].w;
       }
     }
-    const int of_seq = c.row0 + row, src = s_row[c.b] + of_seq / G;
+    const int of_seq = c.row0 + row, query = query_of(of_seq), src = s_row[c.b] + query;
     const float f = s_out[ir];
     if (src >= 0 && src < a.n_q)
-      put(src, c.h * G + of_seq % G, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+      put(src, (c.h - query) * G + of_seq, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
   }
 }
 
