@@ -874,7 +874,7 @@ extern "C" size_t bc_kv8_attention_scratch_bytes(int batch, int n_kv_heads, int 
 extern "C" bc_status bc_kv8_attention(const bc_kv8_attention_args* a, void* stream) {
   const char* who = "bc_kv8_attention";
   if (!a) return entry_fail(BC_EINVAL, "%s: null arguments", who);
-  if (!a->q || !a->out || !a->pool || !a->lens || !a->table || !a->scratch || (a->pages && !a->n_sel))
+  if (!a->q || !a->out || !a->pool || !a->lens || !a->table || !a->scratch || !a->pages != !a->n_sel)
     return entry_fail(BC_EINVAL, "%s: null pointer", who);
   if (a->head_dim != 64 && a->head_dim != 128) return entry_fail(BC_EINVAL, "%s: head_dim must be 64 or 128", who);
   if (!attn8_sizes_ok(a->batch, a->n_kv_heads, a->group, a->max_q, a->head_dim))

@@ -191,8 +191,8 @@ def kv8_attention(q, pool, lens, table, out, scratch, code="e4m3", q_start=None,
     if (pages is None) != (n_sel is None):
         raise ValueError(f"{who}: pages and n_sel go together")
     if pages is not None:
-        if pages.dim() != 3 or pages.shape[0] != B or pages.shape[1] != H:
-            raise ValueError(f"{who}: pages must be [batch][n_kv_heads][max_sel]")
+        if pages.dim() != 3 or pages.shape[0] != B or pages.shape[1] != H or pages.shape[2] == 0:
+            raise ValueError(f"{who}: pages must be [batch][n_kv_heads][max_sel], max_sel at least 1")
         max_sel = pages.shape[2]
     if n_q == 0:
         return

@@ -523,7 +523,8 @@ BC_API bc_status bc_kv8_gather(const void* pool, bc_kv8_type type, int n_pages, 
  *            that is not there
  *   pages, n_sel  optional page lists: [batch][n_kv_heads][max_sel] pages of
  *            the sequence (0 .. ceil(n/16) - 1, ascending, each once), the
- *            first n_sel[b] of each row used; others of a row are skipped
+ *            first n_sel[b] of each row used; others of a row are skipped;
+            max_sel >= 1, and n_sel may be 0 (a list without pages)
  *   scratch  bc_kv8_attention_scratch_bytes(...) bytes, 256-byte aligned:
  *            partial results, a status word and tickets; zero it before the
  *            first call (every call leaves the tickets at zero).  Calls of any

@@ -78,6 +78,11 @@ def test_attention_refuses(over):
     assert bc.bc_last_error()
 
 
+def test_attention_refuses_half_a_page_list():
+    """Without its lists a count is not taken for "every page"."""
+    assert attn(n_sel=P) == bc.BC_EINVAL
+
+
 def test_attention_small_scratch_and_no_rows():
     need = bc.bc_kv8_attention_scratch_bytes(2, 8, 4, 1, 128)
     assert attn(scratch_bytes=need - 1) == bc.BC_ENOMEM

@@ -372,6 +372,21 @@ def test_attention_unequal_value_scales(code):
         assert (np.abs(got - want) <= tol).all(), keep
 
 
+def test_attention_lists_without_pages():
+    """A list of no pages sees nothing; one that could hold none is refused
+    (an empty tensor has no address, which would mean every page)."""
+    pool, q, out = to(DEV, make_pool(4, 1, 64, "int8")), torch.randn(2, 2, 64, generator=gen(1)).to(DEV), \
+        torch.full((2, 2, 64), 7.0, device=DEV)
+    scratch = torch.zeros(bc.bc_kv8_attention_scratch_bytes(2, 1, 2, 1, 64), dtype=torch.uint8, device=DEV)
+    call = lambda pages: bc.kv8_attention(q, pool, ints([20, 40]), ints([[0, 1, 2], [1, 2, 3]]), out, scratch, "int8",
+                                          pages=pages, n_sel=ints([0, 0]))
+    with pytest.raises(ValueError, match="max_sel"):
+        call(torch.zeros(2, 1, 0, dtype=torch.int32, device=DEV))
+    assert (out == 7).all()
+    call(torch.zeros(2, 1, 3, dtype=torch.int32, device=DEV))
+    assert (out == 0).all()
+
+
 def test_attention_not_a_number():
     """A poisoned block reaches the rows of its head that see it, no others."""
     H, G, hd = 2, 2, 64
