@@ -96,6 +96,11 @@ __device__ __forceinline__ float lg2(float x) {          // scales are 0, NaN or
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float min_nan(float x, float y) {       // not a number if either is not
+  float z;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -514,8 +519,9 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     float w[2][2];
     #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      // the bound keeps 0 * f a 0; it is passed only where p is below 2^-96
-      const float f = ex2(fminf(lvs + (m[i] - mo[i]) + kLift, 100.f));
+      // the bound keeps 0 * f a 0; it is passed only where p is below 2^-96.  A
+      // scale that is not a number makes even a weight of 0 one.
+      const float f = ex2(min_nan(lvs + (m[i] - mo[i]) + kLift, 100.f));
       #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float p = ex2(y[i][j]);

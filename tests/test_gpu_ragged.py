@@ -372,10 +372,31 @@ def test_attention_unequal_value_scales(code):
         assert (np.abs(got - want) <= tol).all(), keep
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_attention_value_scale_not_a_number(dtype):
+    """It makes every row that sees the block not a number, whatever the weight
+    and the codes: one token of positive codes, or a weight that is 0 (of
+    sequences so many that a warp reads both pages of some)."""
+    hd, B = 64, 2000
+    k = np.zeros((32, 1, hd), np.float32)
+    k[:16, 0, 0] = 8.0
+    v = np.ones((32, 1, hd), np.float32)
+    pool = np.zeros((2, 1, og.block_bytes(hd)), np.uint8)
+    og.append(pool, k, v, np.arange(32), "e4m3")
+    pool[1, 0, 32 * hd + 4:32 * hd + 8] = np.array([np.nan], np.float32).view(np.uint8)
+    q = torch.zeros(B, 1, hd, dtype=dtype)
+    q[1:, 0, 0] = 8000.0               # the logits of page 0 are 8000 above those of page 1
+    out = torch.empty(B, 1, hd, dtype=dtype, device=DEV)
+    scratch = torch.zeros(bc.bc_kv8_attention_scratch_bytes(B, 1, 1, 1, hd), dtype=torch.uint8, device=DEV)
+    bc.kv8_attention(q.to(DEV), to(DEV, pool), ints([1] + [32] * (B - 1)), ints([[1, 0]] + [[0, 1]] * (B - 1)), out,
+                     scratch, "e4m3")
+    assert torch.isnan(out).all()
+
+
 def test_attention_lists_without_pages():
     """A list of no pages sees nothing; one that could hold none is refused
     (an empty tensor has no address, which would mean every page)."""
-    pool, q, out = to(DEV, make_pool(4, 1, 64, "int8")), torch.randn(2, 2, 64, generator=gen(1)).to(DEV), \
+    pool, q, out = to(DEV, make_pool(4, 1, 64, "int8", seed=1)), torch.randn(2, 2, 64, generator=gen(1)).to(DEV), \
         torch.full((2, 2, 64), 7.0, device=DEV)
     scratch = torch.zeros(bc.bc_kv8_attention_scratch_bytes(2, 1, 2, 1, 64), dtype=torch.uint8, device=DEV)
     call = lambda pages: bc.kv8_attention(q, pool, ints([20, 40]), ints([[0, 1, 2], [1, 2, 3]]), out, scratch, "int8",
