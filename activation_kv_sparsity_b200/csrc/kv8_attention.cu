@@ -902,8 +902,10 @@ extern "C" bc_status bc_kv8_attention(const bc_kv8_attention_args* a, void* stre
   if (a->q_stride % 8 || a->q_stride < (long long)a->n_kv_heads * a->group * a->head_dim)
     return entry_fail(BC_EINVAL, "%s: q_stride must be a multiple of 8 and cover the heads", who);
   if (!aligned(a->scratch, 256)) return entry_fail(BC_EINVAL, "%s: scratch must be 256-byte aligned", who);
-  if (!(a->cap >= 0.f && a->cap <= 3.4e38f) || a->window < 0 || !(fabsf(a->scale) <= 3.4e38f))
-    return entry_fail(BC_EINVAL, "%s: cap and window must not be negative, cap and scale finite", who);
+  // a cap below the normal range has no finite reciprocal
+  if (!(a->cap == 0.f || (a->cap >= 1.17549435e-38f && a->cap <= 3.4e38f)) || a->window < 0 ||
+      !(fabsf(a->scale) <= 3.4e38f))
+    return entry_fail(BC_EINVAL, "%s: cap must be 0 or a positive normal number, window not negative, scale finite", who);
   if (a->scratch_bytes < bc_kv8_attention_scratch_bytes(a->batch, a->n_kv_heads, a->group, a->max_q, a->head_dim))
     return entry_fail(BC_ENOMEM, "%s: scratch too small", who);
   if (a->n_q == 0) return BC_OK;

@@ -551,7 +551,7 @@ typedef struct {
   const int* pages;      /* [batch][n_kv_heads][max_sel] or NULL */
   const int* n_sel;      /* [batch], with pages */
   float scale;           /* of q . k; usually 1 / sqrt(head_dim) */
-  float cap;             /* 0: none */
+  float cap;             /* 0: none; else a normal number */
   int window;            /* 0: none */
   const float* slopes;   /* [n_kv_heads * group] or NULL */
   void* scratch;

@@ -72,7 +72,7 @@ def attn(**over):
                           dict(pages=P, n_sel=P, max_sel=0), dict(q=264), dict(out=264), dict(pool=264),
                           dict(scratch=272), dict(cap=-1.0), dict(cap=float("nan")), dict(window=-1),
                           dict(scale=float("nan")), dict(scale=float("inf")),
-                          dict(cap=float("inf"))])
+                          dict(cap=float("inf")), dict(cap=1e-39)])
 def test_attention_refuses(over):
     assert attn(**over) == bc.BC_EINVAL
     assert bc.bc_last_error()
