@@ -68,6 +68,12 @@ def _pool(who, pool):
     return P, H, _BLOCKS[block], pool.get_device()
 
 
+def _fits(who, *ints):
+    """The argument blocks hold 32-bit integers; ctypes would cut longer ones."""
+    if max(ints) > 0x7fffffff or min(ints) < -0x80000000:
+        raise ValueError(f"{who}: a size beyond 2^31 - 1 ({ints})")
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -102,6 +108,7 @@ def block_tables(lens, delta, table, free_list, n_free, lens_out, n_free_out, q_
                ticket=ticket)
         _sizes(who, lens=(lens, B), delta=(delta, B), lens_out=(lens_out, B), q_start=(q_start, B + 1),
                n_free=(n_free, 1), n_free_out=(n_free_out, 1), ticket=(ticket, 1), positions=(positions, n))
+    _fits(who, B, max_blocks, n_pages, n)
     a = bc_block_tables_args(B, max_blocks, n_pages, n, lens.data_ptr(), delta.data_ptr(),
                              table.data_ptr(), free_list.data_ptr(), n_free.data_ptr(), lens_out.data_ptr(),
                              n_free_out.data_ptr(), q_start.data_ptr(), slots.data_ptr(), positions.data_ptr(),
@@ -194,6 +201,7 @@ def kv8_attention(q, pool, lens, table, out, scratch, code="e4m3", q_start=None,
         if pages.dim() != 3 or pages.shape[0] != B or pages.shape[1] != H or pages.shape[2] == 0:
             raise ValueError(f"{who}: pages must be [batch][n_kv_heads][max_sel], max_sel at least 1")
         max_sel = pages.shape[2]
+    _fits(who, n_q, B, max_blocks, max_sel, max_q, window)
     if n_q == 0:
         return
     a = bc_kv8_attention_args(q.data_ptr(), out.data_ptr(), dt, q.stride(0) if n_q > 1 else Hq * hd, n_q,
@@ -234,6 +242,8 @@ def logits_adjust(logits, out, hist=None, hist_start=None, prompt_len=None, repe
         if mask.dim() != 2 or mask.shape[1] != (V + 31) // 32:
             raise ValueError(f"{who}: mask must be [n_masks][{(V + 31) // 32}]")
         n_masks = mask.shape[0]
+        if mask_row is None and B > n_masks == 0:       # an empty tensor has no address: no masks at all
+            raise ValueError(f"{who}: without mask_row there is a mask for each of the {B} rows, not 0")
     if not ((hist is None or (_is(hist, _I32, dev, n_hist) and _is(hist_start, _I32, dev, B + 1)))
             and (bias_ids is None or (_is(bias_ids, _I32, dev, n_bias) and _is(bias_vals, _F32, dev, n_bias)
                                       and _is(bias_start, _I32, dev, B + 1)))
@@ -249,6 +259,7 @@ def logits_adjust(logits, out, hist=None, hist_start=None, prompt_len=None, repe
         _sizes(who, hist_start=(hist_start, B + 1), bias_start=(bias_start, B + 1), prompt_len=(prompt_len, B),
                mask_row=(mask_row, B), repetition=(repetition, B), frequency=(frequency, B), presence=(presence, B),
                bias_vals=(bias_vals, n_bias))
+    _fits(who, B, V, n_hist, n_bias, n_masks)
     if B == 0 or V == 0:
         return
     a = bc_logits_args(logits.data_ptr(), out.data_ptr(), dt, B, V, logits.stride(0) if B > 1 else V,

@@ -808,3 +808,29 @@ def test_outputs_beyond_2_31_elements():
     want = torch.full((V,), 2.0)
     want[5], want[V - 1] = 0.5, 0.75
     assert torch.equal(x[-1].float().cpu(), want)
+
+
+def test_wrappers_refuse_sizes_beyond_32_bits():
+    """They would reach the C interface cut to their lower 32 bits."""
+    pool, q = to(DEV, make_pool(2, 1, 64, "e4m3", seed=1)), torch.zeros(1, 1, 64, device=DEV)
+    out = torch.full_like(q, 7.0)
+    scratch = torch.zeros(bc.bc_kv8_attention_scratch_bytes(1, 1, 1, 1, 64), dtype=torch.uint8, device=DEV)
+    for kw in (dict(window=2 ** 32 + 8), dict(window=-2 ** 32 + 8), dict(q_start=ints([0, 1]), max_q=2 ** 32 + 1)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            bc.kv8_attention(q, pool, ints([20]), ints([[0, 1]]), out, scratch, "e4m3", **kw)
+    lg = torch.full((1, 40), 7.0, device=DEV)
+    if torch.cuda.mem_get_info()[0] > 24 << 30:
+        with pytest.raises(ValueError, match="2\\^31"):
+            bc.logits_adjust(lg, lg, hist=torch.empty(2 ** 32 + 4, dtype=torch.int32, device=DEV), hist_start=ints([0, 4]))
+        torch.cuda.empty_cache()
+    assert (out == 7).all() and (lg == 7).all()
+
+
+@pytest.mark.parametrize("n_masks", [0, 1])
+def test_logits_refuse_fewer_masks_than_rows(n_masks):
+    lg = torch.full((2, 40), 7.0, device=DEV)
+    with pytest.raises((ValueError, bc.BCError), match="mask for each|n_masks"):
+        bc.logits_adjust(lg, lg, mask=torch.zeros(n_masks, 2, dtype=torch.int32, device=DEV))
+    # with mask_row a row outside them has none
+    bc.logits_adjust(lg, lg, mask=torch.zeros(n_masks, 2, dtype=torch.int32, device=DEV), mask_row=ints([n_masks, -1]))
+    assert (lg == 7).all()
