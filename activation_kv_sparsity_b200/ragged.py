@@ -317,13 +317,13 @@ class RaggedCache:
 
     def read(self, layer: int, seq: int, n: int, dtype=torch.bfloat16):
         """The first n tokens of a sequence as (k, v), each [n][n_kv_heads][hd],
-        on the current stream."""
+        on the current stream; zeros behind its last one."""
         H, hd = self.pool.shape[2], (self.pool.shape[3] - 32) // 32
         if not 0 <= n <= 16 * self.table.shape[1]:
             raise ValueError("RaggedCache.read: n outside the sequence's table")
         dev = self.pool.device
         pos = torch.arange(n, device=dev)
-        slots = (self.table[seq][pos // 16] * 16 + pos % 16).int()
+        slots = torch.where(pos < self.lens[seq], self.table[seq][pos // 16] * 16 + pos % 16, -1).int()
         k = torch.empty(n, H, hd, dtype=dtype, device=dev)
         v = torch.empty_like(k)
         kv8_gather(self._pools[layer], slots, k, v, self.code)

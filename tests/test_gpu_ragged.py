@@ -834,3 +834,18 @@ def test_logits_refuse_fewer_masks_than_rows(n_masks):
     # with mask_row a row outside them has none
     bc.logits_adjust(lg, lg, mask=torch.zeros(n_masks, 2, dtype=torch.int32, device=DEV), mask_row=ints([n_masks, -1]))
     assert (lg == 7).all()
+
+
+def test_read_stops_at_the_end_of_a_sequence():
+    """Entries of the table behind a sequence's pages are old or zero: the
+    pages of others."""
+    c = bc.RaggedCache(1, 2, 8, 1, 1, 64, 4, 64, code="int8", device=DEV)
+    c.plan(ints([20, 30]))
+    x = torch.randn(64, 1, 64, generator=gen(3)).to(DEV)
+    c.append(0, x, x + 1)
+    c.plan(ints([-3, 0]))
+    k, v = c.read(0, 0, 60, torch.float32)
+    # int8 codes of one scale a page: half a step of max / 127, twice where the scale grew
+    step = float((x.abs().max() + 1) / 127)
+    assert (k[:17] - x[:17]).abs().max() <= step and (v[:17] - x[:17] - 1).abs().max() <= step
+    assert (k[17:] == 0).all() and (v[17:] == 0).all()
