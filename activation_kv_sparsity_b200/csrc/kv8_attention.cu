@@ -298,8 +298,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   // block number page * H + h and the page of the sequence, or -1 (not there).
   auto lookup = [&](int k, int& entry, int& logical) {
     entry = logical = -1;
+    if (k >= g1 - g0) return;                    // (g0 + k might pass an int)
     const int u = g0 + k;
-    if (u >= g1) return;
     int b, h, tile, begin, end;
     locate(u, b, h, tile, begin, end);
     if (a.pages) {
@@ -683,6 +683,12 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   #pragma unroll 1
   for (int k = 0;; ++k) {
     if (k == n_units || g0 + k == seg_end) {
+      if (k == n_units && gave_up >= 0) {
+        if (lane == 0) atomicOr(ga.status, 1u);
+        // copies still in flight land before the ring is used again
+        for (int i = max(0, gave_up - kA8Ring); i < gave_up; ++i)
+          mbar_wait(full0 + 8 * (i & (kA8Ring - 1)), (i / kA8Ring) & 1);
+      }
       if (k > 0) {
         const bool head = my_seg->begin < g0;
         float* dst = head ? my_head : nullptr;
@@ -710,11 +716,6 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     if (gave_up < 0 && lp >= 0) process(my_ring + stage * BLK, lp);
     __syncwarp();
     if (k + kA8Ring < n_units && gave_up < 0) issue(k + kA8Ring);
-  }
-  if (gave_up >= 0) {
-    if (lane == 0) atomicOr(ga.status, 1u);
-    // copies still in flight land before the ring is used again
-    for (int i = max(0, gave_up - kA8Ring); i < gave_up; ++i) mbar_wait(full0 + 8 * (i & (kA8Ring - 1)), (i / kA8Ring) & 1);
   }
   __syncthreads();
 

@@ -131,11 +131,7 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas) k_logits(const __gr
       inv_rep = __frcp_rn(rep);                 // x / rep to within an ulp and a half, for one multiplication an id
       freq = a.frequency ? a.frequency[row] : 0.f;
       pres = a.presence ? a.presence[row] : 0.f;
-      mask = nullptr;
-      if (a.mask) {
-        const int m = a.mask_row ? a.mask_row[row] : row;
-        if (m >= 0 && m < a.n_masks) mask = a.mask + (size_t)m * ((a.vocab + 31) / 32);
-      }
+      mask = mask_of(a, row);
       nh = min(h1 - h0, kLogitList);
       const int pad = (nh + 3) & ~3;
       nb = min(b1 - b0, kLogitList - pad);
