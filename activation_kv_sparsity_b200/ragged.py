@@ -80,7 +80,7 @@ def _ptr(t):
 
 def _call(dev, stream, where, fn, *args):
     """fn(*args, stream) with device number dev current."""
-    if torch.cuda.current_device() != dev:
+    if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return _call(dev, stream, where, fn, *args)
     s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
