@@ -1,19 +1,24 @@
 // Penalties, biases and grammar masks on logits (bc_logits_adjust): one pass
 // over the logits, HBM-bound.
 //
-// Persistent CTAs take pieces of 2048 to 8192 ids, neighbours of a row one
-// after the other, and load a piece's logits (4 a thread and round) while the
-// one before is worked on.  A row's history and biases are read once per row
-// and CTA into shared memory.  For each piece the CTA walks them and marks the
-// ids that fall into the piece, a word per id and list; each thread then looks
-// its own ids up and clears their words.  A word of the history is bit 31,
-// "seen in the prompt", and the count of the output tokens; a word of the
-// biases the place of the last entry for the id (a maximum), so no result
-// depends on the order of the atomics.
+// Persistent CTAs take pieces of at most 8192 ids, neighbours of a row one
+// after the other, and load a piece's logits (16 bytes a thread and round, as
+// they are: a conversion on the way would wait for them) while the one before
+// is worked on.  A row's history and biases are read once per row and CTA into
+// shared memory.  For each piece the CTA walks them and marks the ids that fall
+// into the piece, a word per id and list; each thread then looks its own ids up
+// and clears their words.  A word of the history is bit 31, "seen in the
+// prompt", and the count of the output tokens; a word of the biases the place of
+// the last entry for the id (a maximum), so no result depends on the order of
+// the atomics.
 // 160 rows of 128256 f32 logits with histories of up to 8192 tokens, 32 biases
-// and masks take 46 us (3.5 TB/s of logits; 29 us without lists, the copy's
-// rate); 68 us with a CTA a piece that walks the lists in L2, 55 us as a copy
-// and a scatter from hash tables.  The walks' instructions bound the rest.
+// and masks take 41 us (4.0 TB/s of logits), 34 us with histories of up to 1000
+// tokens, 29 us with neither lists nor masks (5.7 TB/s, the copy's rate); in
+// bf16 36, 27 and 17 us.  What the lists cost is the walks and the barriers
+// around them.  Slower were a CTA a piece that walks the lists in L2 (68 us) and a
+// copy and a scatter from hash tables (55); pieces in shared memory by
+// asynchronous copies leave the lists too little room, and cutting a row's list to
+// the CTA's own ids takes longer than the walks that it shortens.
 #include "common.cuh"
 #include "entry.h"
 
@@ -23,32 +28,48 @@
 namespace bc {
 
 constexpr int kLogitThreads = 512;
-constexpr int kLogitRound = 4 * kLogitThreads;   // ids per round
-constexpr int kLogitRounds = 4;                  // at most, per piece
 constexpr int kLogitCtas = 2;                    // per SM
-constexpr int kLogitList = 8192;                 // list entries in shared memory
 constexpr int kLogitWalk = 8;                    // further ones per thread in flight
+
+// A piece: at most kRounds times 16 bytes a thread, held in registers.  Its two
+// arrays of marks and the lists fill half an SM's shared memory.
+template <typename T>
+struct LogitPiece {
+  static constexpr int kVec = 16 / sizeof(T);
+  static constexpr int kRound = kLogitThreads * kVec;
+  static constexpr int kRounds = sizeof(T) == 4 ? 4 : 2;
+  static constexpr int kIds = kRound * kRounds;
+  static constexpr int kList = 8192;               // list entries in shared memory
+  static constexpr int kSmem = 8 * kIds + 4 * kList;
+};
 
 struct LogitsArgs {
   bc_logits_args a;
-  int rounds;                 // of kLogitRound ids per piece
+  int rounds;                 // of 16 bytes a thread per piece
   int pieces;                 // per row
   long long items, per_cta;   // pieces in all, and per CTA
 };
 
-__device__ __forceinline__ float4 load_four(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load_four(const __nv_bfloat16* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-}
-__device__ __forceinline__ void store_four(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
-__device__ __forceinline__ void store_four(__nv_bfloat16* p, float4 x) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-}
 __device__ __forceinline__ float value_of(float x) { return x; }
 __device__ __forceinline__ float value_of(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void store_one(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_one(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// 16 bytes of logits with those whose bit is 0 at -inf
+template <typename T>
+__device__ __forceinline__ uint4 masked(uint4 w, uint32_t bits) {
+  uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  #pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (sizeof(T) == 4) {
+      if (!(bits >> i & 1u)) x[i] = 0xff800000u;
+    } else {
+      const uint32_t keep = (bits >> (2 * i) & 1u ? 0xffffu : 0u) | (bits >> (2 * i + 1) & 1u ? 0xffff0000u : 0u);
+      x[i] = (x[i] & keep) | (0xff80ff80u & ~keep);
+    }
+  }
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
 
 // Shared-memory atomics under a predicate, without a branch: most entries of a
 // list are not of the piece at hand.
@@ -76,41 +97,69 @@ __device__ __forceinline__ const uint32_t* mask_of(const bc_logits_args& a, int 
 
 template <typename T>
 __global__ void __launch_bounds__(kLogitThreads, kLogitCtas) k_logits(const __grid_constant__ LogitsArgs g) {
-  extern __shared__ __align__(16) unsigned s_mark[];            // [kLogitRounds * kLogitRound]
-  unsigned* s_bias = s_mark + kLogitRounds * kLogitRound;       // the same for the biases
-  int* s_list = reinterpret_cast<int*>(s_bias + kLogitRounds * kLogitRound);
-  // [kLogitList]: history, then biases, each padded to a multiple of 4
+  using P = LogitPiece<T>;
+  constexpr int VEC = P::kVec;
+  extern __shared__ __align__(16) uint8_t smem[];
+  unsigned* s_mark = reinterpret_cast<unsigned*>(smem);               // [kIds] of the history
+  unsigned* s_bias = s_mark + P::kIds;                                // [kIds] of the biases
+  int* s_list = reinterpret_cast<int*>(s_bias + P::kIds);
+  // [kList]: history, then biases, each padded to a multiple of 4
   const bc_logits_args& a = g.a;
-  const int piece = g.rounds * kLogitRound;
+  const int piece = g.rounds * P::kRound;
   const long long first = blockIdx.x * g.per_cta;
   int left = (int)min(g.per_cta, g.items - first);
   pdl_wait();
   pdl_trigger();
   if (left <= 0) return;
 
-  int row = (int)(first / g.pieces), v0 = (int)(first % g.pieces) * piece;
-  // rows of any alignment: four at a time where both sides allow it
-  auto load = [&](float (&x)[kLogitRounds][4], int r, int v) {
-    const T* src = static_cast<const T*>(a.logits) + (long long)r * a.stride + v;
-    const int n = min(piece, a.vocab - v);
-    const bool wide = (reinterpret_cast<uintptr_t>(src) & (4 * sizeof(T) - 1)) == 0;
+  // A piece of a row holds its ids from lo on, lo at a 16-byte boundary of the
+  // logits (the first one begins up to VEC - 1 places before the row); those at
+  // its places t0 .. t1 - 1 exist.
+  struct Piece {
+    int row, lo, t0, t1;
+    const T* src;             // place 0 of it
+    T* dst;
+  };
+  auto begin_row = [&](int row) {
+    Piece x;
+    x.row = row;
+    x.src = static_cast<const T*>(a.logits) + (long long)row * a.stride;
+    x.dst = static_cast<T*>(a.out) + (long long)row * a.out_stride;
+    x.t0 = (int)(reinterpret_cast<uintptr_t>(x.src) % 16 / sizeof(T));
+    x.lo = -x.t0;
+    x.src -= x.t0;
+    x.dst -= x.t0;
+    x.t1 = min(piece, a.vocab - x.lo);
+    return x;
+  };
+  auto move = [&](Piece& x, int by) {              // within the row
+    x.lo += by;
+    x.src += by;
+    x.dst += by;
+    x.t0 = 0;
+    x.t1 = min(piece, a.vocab - x.lo);
+  };
+  auto fetch = [&](uint4 (&w)[P::kRounds], const Piece& x) {
     #pragma unroll
-    for (int k = 0; k < kLogitRounds; ++k) {
-      const int i = k * kLogitRound + 4 * threadIdx.x;
-      if (wide && i + 4 <= n) {
-        const float4 y = load_four(src + i);
-        x[k][0] = y.x; x[k][1] = y.y; x[k][2] = y.z; x[k][3] = y.w;
-      } else {
+    for (int r = 0; r < P::kRounds; ++r) {
+      const int t = r * P::kRound + VEC * threadIdx.x;
+      if (t >= x.t0 && t + VEC <= x.t1) {
+        w[r] = *reinterpret_cast<const uint4*>(x.src + t);
+      } else if (t < x.t1 && t + VEC > x.t0) {
+        T* y = reinterpret_cast<T*>(&w[r]);
         #pragma unroll
-        for (int j = 0; j < 4; ++j) x[k][j] = i + j < n ? value_of(src[i + j]) : 0.f;
+        for (int j = 0; j < VEC; ++j)
+          if (t + j >= x.t0 && t + j < x.t1) y[j] = x.src[t + j];
       }
     }
   };
-  float x[kLogitRounds][4], next[kLogitRounds][4];
-  load(x, row, v0);
-  #pragma unroll
-  for (int k = 0; k < 2 * kLogitRounds; ++k)
-    *reinterpret_cast<uint4*>(s_mark + k * kLogitRound + 4 * threadIdx.x) = make_uint4(0, 0, 0, 0);
+  int p = (int)(first % g.pieces);
+  Piece x = begin_row((int)(first / g.pieces));
+  if (p) move(x, p * piece);
+  uint4 w[P::kRounds], w_next[P::kRounds];
+  fetch(w, x);
+  for (int i = 4 * threadIdx.x; i < 2 * P::kIds; i += 4 * kLogitThreads)
+    *reinterpret_cast<uint4*>(s_mark + i) = make_uint4(0, 0, 0, 0);
 
   int at_row = -1, h0 = 0, h1 = 0, b0 = 0, b1 = 0, nh = 0, nb = 0;   // nh, nb: entries in shared memory
   unsigned out0 = 0;
@@ -118,10 +167,8 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas) k_logits(const __gr
   const uint32_t* mask = nullptr;
   for (;;) {
     const bool more = --left > 0;
-    const int next_row = v0 + piece < a.vocab ? row : row + 1, next_v0 = v0 + piece < a.vocab ? v0 + piece : 0;
-    if (more) load(next, next_row, next_v0);
-    if (row != at_row) {
-      at_row = row;
+    if (x.row != at_row) {
+      const int row = at_row = x.row;
       h0 = a.hist ? clamp_at(a.hist_start[row], a.n_hist) : 0;
       h1 = max(h0, a.hist ? clamp_at(a.hist_start[row + 1], a.n_hist) : 0);
       b0 = a.bias_ids ? clamp_at(a.bias_start[row], a.n_bias) : 0;
@@ -132,37 +179,65 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas) k_logits(const __gr
       freq = a.frequency ? a.frequency[row] : 0.f;
       pres = a.presence ? a.presence[row] : 0.f;
       mask = mask_of(a, row);
-      nh = min(h1 - h0, kLogitList);
+      nh = min(h1 - h0, P::kList);
       const int pad = (nh + 3) & ~3;
-      nb = min(b1 - b0, kLogitList - pad);
+      nb = min(b1 - b0, P::kList - pad);
       __syncthreads();                          // the list of the row before is done with
       // asynchronous copies: a thread's entries are all in flight at once
-      auto fetch = [&](const int* list, int count, int* to) {
+      auto bring = [&](const int* list, int count, int* to) {
         for (int i = threadIdx.x; i < count; i += kLogitThreads)
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(to + i)), "l"(list + i) : "memory");
         if (threadIdx.x < (-count & 3)) to[count + threadIdx.x] = -1;
       };
-      fetch(a.hist + h0, nh, s_list);
-      fetch(a.bias_ids + b0, nb, s_list + pad);
+      bring(a.hist + h0, nh, s_list);
+      bring(a.bias_ids + b0, nb, s_list + pad);
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncthreads();
     }
-    const int n = min(piece, a.vocab - v0);
-    uint32_t bits[kLogitRounds];                 // on their way during the walks
-    #pragma unroll
-    for (int k = 0; k < kLogitRounds; ++k) {
-      const int i = k * kLogitRound + 4 * threadIdx.x;
-      bits[k] = mask && i < n ? mask[(v0 + i) >> 5] >> (i & 31) : 0xfu;
+    const int v0 = x.lo + x.t0;
+    const unsigned n = max(x.t1 - x.t0, 0);      // (a row's last piece may hold nothing)
+    unsigned *mark0 = s_mark + x.t0, *bias0 = s_bias + x.t0;
+    Piece next = x;                              // on its way until then
+    if (more) {
+      if (++p < g.pieces) {
+        move(next, piece);
+      } else {
+        p = 0;
+        next = begin_row(x.row + 1);
+      }
+      fetch(w_next, next);
     }
-    // mark(i, ids - v0, step) for the entries of
-    // list[begin, stop), its first `held` entries at s_list[from]; four at a
-    // time: entries i, i + step, ..
-    auto walk = [&](const int* list, int begin, int stop, int from, int held, auto mark) {
-      for (int i = 4 * threadIdx.x; i < held; i += kLogitRound) {
+    uint32_t bits[P::kRounds];                   // on their way during the walks
+    #pragma unroll
+    for (int r = 0; r < P::kRounds; ++r) bits[r] = 0xffu;
+    // The usual case: 16 bytes are of one word.  It is shifted where it is used,
+    // so that nothing waits for it before the walks (44 against 47 us).
+    const bool in_word = x.lo % 32 == 0;
+    if (mask && in_word) {
+      const uint32_t* m = mask + (x.lo >> 5);
+      #pragma unroll
+      for (int r = 0; r < P::kRounds; ++r) {
+        const int t = r * P::kRound + VEC * threadIdx.x;
+        if (t < x.t1) bits[r] = m[t >> 5];
+      }
+    } else if (mask) {
+      #pragma unroll
+      for (int r = 0; r < P::kRounds; ++r) {
+        const int t = r * P::kRound + VEC * threadIdx.x;
+        if (t >= x.t1 || t + VEC <= x.t0) continue;
+        const int v = max(x.lo + t, 0), e = min(x.lo + t + VEC, a.vocab) - 1;    // first and last id of the 16 bytes
+        const uint32_t m0 = mask[v >> 5], m1 = (e ^ v) >> 5 ? mask[e >> 5] : 0u;
+        bits[r] = __funnelshift_r(m0, m1, v & 31) << (v - (x.lo + t));
+      }
+    }
+    // use(i, ids - v0, step) for the entries of list[begin, stop), its first
+    // `held` entries at s_list[from]; four at a time: entries i, i + step, ..
+    auto walk = [&](const int* list, int begin, int stop, int from, int held, auto use) {
+      for (int i = 4 * threadIdx.x; i < held; i += 4 * kLogitThreads) {
         const int4 id = *reinterpret_cast<const int4*>(s_list + from + i);
         const unsigned v[4] = {(unsigned)id.x - (unsigned)v0, (unsigned)id.y - (unsigned)v0, (unsigned)id.z - (unsigned)v0,
                                (unsigned)id.w - (unsigned)v0};
-        mark((unsigned)(begin + i), v, 1u);
+        use((unsigned)(begin + i), v, 1u);
       }
       for (unsigned i0 = begin + held + threadIdx.x; i0 < (unsigned)stop; i0 += kLogitWalk * kLogitThreads) {
         unsigned v[kLogitWalk];
@@ -172,85 +247,84 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas) k_logits(const __gr
           v[j] = i < (unsigned)stop ? (unsigned)list[i] - (unsigned)v0 : 0xffffffffu;
         }
         #pragma unroll
-        for (int j = 0; j < kLogitWalk; j += 4) mark(i0 + j * kLogitThreads, v + j, (unsigned)kLogitThreads);
+        for (int j = 0; j < kLogitWalk; j += 4) use(i0 + j * kLogitThreads, v + j, (unsigned)kLogitThreads);
       }
     };
-    if (h1 > h0) {
+    const bool listed = h1 > h0 || b1 > b0;
+    if (listed) {
       walk(a.hist, h0, h1, 0, nh, [&](unsigned i, const unsigned* v, unsigned step) {
         if (i >= out0) {
           #pragma unroll
-          for (int j = 0; j < 4; ++j) add_if(s_mark + v[j], 1u, v[j] < (unsigned)n);
+          for (int j = 0; j < 4; ++j) add_if(mark0 + v[j], 1u, v[j] < n);
+        } else if (i + 3 * step < out0) {
+          #pragma unroll
+          for (int j = 0; j < 4; ++j) or_if(mark0 + v[j], 0x80000000u, v[j] < n);
         } else {
           #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const bool prompt = i + j * step < out0;
-            or_if(s_mark + v[j], 0x80000000u, prompt && v[j] < (unsigned)n);
-            add_if(s_mark + v[j], 1u, !prompt && v[j] < (unsigned)n);
+            or_if(mark0 + v[j], 0x80000000u, prompt && v[j] < n);
+            add_if(mark0 + v[j], 1u, !prompt && v[j] < n);
           }
         }
       });
-    }
-    if (b1 > b0) {
-      walk(a.bias_ids, b0, b1, (nh + 3) & ~3, nb,
-           [&](unsigned i, const unsigned* v, unsigned step) {
-             #pragma unroll
-             for (int j = 0; j < 4; ++j) max_if(s_bias + v[j], i + j * step - b0 + 1, v[j] < (unsigned)n);
-           });
-    }
-    if (h1 > h0 || b1 > b0) {
+      walk(a.bias_ids, b0, b1, (nh + 3) & ~3, nb, [&](unsigned i, const unsigned* v, unsigned step) {
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) max_if(bias0 + v[j], i + j * step - b0 + 1, v[j] < n);
+      });
       __syncthreads();
-      // the thread's marked ids, whose words are cleared
+    }
+    // the marked ids among the 16 bytes at place t, whose words are cleared;
+    // four at a time without branches, since most warps find some of a long
+    // history (42 against 44 us)
+    auto change = [&](uint4& at_t, int t) {
+      T* y = reinterpret_cast<T*>(&at_t);
       #pragma unroll
-      for (int k = 0; k < kLogitRounds; ++k) {
-        const int i = k * kLogitRound + 4 * threadIdx.x;
-        if (i >= n) break;
-        const uint4 c4 = *reinterpret_cast<const uint4*>(s_mark + i);
-        if (c4.x | c4.y | c4.z | c4.w) {
-          *reinterpret_cast<uint4*>(s_mark + i) = make_uint4(0, 0, 0, 0);
-          const unsigned c[4] = {c4.x, c4.y, c4.z, c4.w};
-          #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (!c[j]) continue;
-            x[k][j] *= x[k][j] > 0.f ? inv_rep : rep;
-            if (c[j] & 0x7fffffffu) x[k][j] -= __fmul_rn(freq, (float)(c[j] & 0x7fffffffu)) + pres;
-          }
+      for (int q = 0; q < VEC; q += 4) {
+        uint4* mark = reinterpret_cast<uint4*>(s_mark + t + q);
+        uint4* bias = reinterpret_cast<uint4*>(s_bias + t + q);
+        const uint4 c4 = *mark, w4 = b1 > b0 ? *bias : make_uint4(0, 0, 0, 0);
+        if (!(c4.x | c4.y | c4.z | c4.w | w4.x | w4.y | w4.z | w4.w)) continue;
+        *mark = *bias = make_uint4(0, 0, 0, 0);
+        const unsigned c[4] = {c4.x, c4.y, c4.z, c4.w}, at[4] = {w4.x, w4.y, w4.z, w4.w};
+        float z[4];
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const unsigned outputs = c[j] & 0x7fffffffu;
+          const float u = value_of(y[q + j]), f = u > 0.f ? inv_rep : rep;
+          const float off = outputs ? __fmul_rn(freq, (float)outputs) + pres : 0.f;
+          z[j] = c[j] ? __fmul_rn(u, f) - off : u;
         }
-        if (b1 == b0) continue;
-        const uint4 w4 = *reinterpret_cast<const uint4*>(s_bias + i);
         if (w4.x | w4.y | w4.z | w4.w) {
-          *reinterpret_cast<uint4*>(s_bias + i) = make_uint4(0, 0, 0, 0);
-          const unsigned w[4] = {w4.x, w4.y, w4.z, w4.w};
           #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (w[j]) x[k][j] += a.bias_vals[b0 + w[j] - 1];
+            if (at[j]) z[j] += a.bias_vals[b0 + at[j] - 1];
         }
-      }
-      __syncthreads();
-    }
-    T* dst = static_cast<T*>(a.out) + (long long)row * a.out_stride + v0;
-    const bool wide = (reinterpret_cast<uintptr_t>(dst) & (4 * sizeof(T) - 1)) == 0;
-    #pragma unroll
-    for (int k = 0; k < kLogitRounds; ++k) {
-      const int i = k * kLogitRound + 4 * threadIdx.x;
-      if (i >= n) break;
-      #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (!(bits[k] >> j & 1u)) x[k][j] = -INFINITY;
-      if (wide && i + 4 <= n) {
-        store_four(dst + i, make_float4(x[k][0], x[k][1], x[k][2], x[k][3]));
-      } else {
         #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (i + j < n) store_one(dst + i + j, x[k][j]);
+        for (int j = 0; j < 4; ++j) store_one(y + q + j, z[j]);
+      }
+    };
+    const bool wide = reinterpret_cast<uintptr_t>(x.dst) % 16 == 0;
+    #pragma unroll
+    for (int r = 0; r < P::kRounds; ++r) {
+      const int t = r * P::kRound + VEC * threadIdx.x;
+      if (t >= x.t1 || t + VEC <= x.t0) continue;
+      if (listed) change(w[r], t);
+      if (mask) w[r] = masked<T>(w[r], bits[r] >> (in_word ? t & 31 : 0));
+      if (wide && t >= x.t0 && t + VEC <= x.t1) {
+        *reinterpret_cast<uint4*>(x.dst + t) = w[r];
+      } else {
+        const T* y = reinterpret_cast<const T*>(&w[r]);
+        #pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          if (t + j >= x.t0 && t + j < x.t1) x.dst[t + j] = y[j];
       }
     }
     if (!more) break;
-    row = next_row;
-    v0 = next_v0;
+    if (listed) __syncthreads();                 // the marks are clear
+    x = next;
     #pragma unroll
-    for (int k = 0; k < kLogitRounds; ++k)
-      #pragma unroll
-      for (int j = 0; j < 4; ++j) x[k][j] = next[k][j];
+    for (int r = 0; r < P::kRounds; ++r) w[r] = w_next[r];
   }
 }
 
@@ -260,7 +334,7 @@ using namespace bc;
 
 template <typename T>
 static cudaError_t launch_logits(const LogitsArgs& g, dim3 grid, cudaStream_t st) {
-  constexpr int smem = 4 * (2 * kLogitRounds * kLogitRound + kLogitList);
+  constexpr int smem = LogitPiece<T>::kSmem;
   static std::atomic<unsigned long long> ready{0};     // once per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -292,16 +366,26 @@ extern "C" bc_status bc_logits_adjust(const bc_logits_args* a, void* stream) {
     return entry_fail(BC_EINVAL, "%s: n_masks must cover the batch without mask_row", who);
   LogitsArgs g{*a, 1, 0, 0, 0};
   constexpr int kCtas = 148 * kLogitCtas;
-  // pieces no smaller than give every CTA one: each walks the lists
-  const long long per = (long long)kCtas * kLogitRound;
-  g.rounds = (int)std::min<long long>(kLogitRounds, ((long long)a->batch * a->vocab + per - 1) / per);
-  const int piece = g.rounds * kLogitRound;
-  g.pieces = (int)((a->vocab + (long long)piece - 1) / piece);
+  const bool f32 = a->dtype == BC_F32;
+  const int vec = f32 ? LogitPiece<float>::kVec : LogitPiece<__nv_bfloat16>::kVec;
+  const int round = kLogitThreads * vec, most = f32 ? LogitPiece<float>::kRounds : LogitPiece<__nv_bfloat16>::kRounds;
+  // the rounds that take least, at one more per piece for the walks: fewer
+  // where a CTA would get a second piece for want of others (16 rows 7.8 us)
+  long long best = 0;
+  for (int r = 1; r <= most; ++r) {
+    // (a row may begin off a boundary)
+    const long long pieces = (a->vocab + (long long)(vec - 1) + r * round - 1) / (r * round);
+    const long long cost = (a->batch * pieces + kCtas - 1) / kCtas * (r + 1);
+    if (r > 1 && cost > best) continue;
+    best = cost;
+    g.rounds = r;
+    g.pieces = (int)pieces;
+  }
   g.items = (long long)a->batch * g.pieces;
   const long long ctas = std::min<long long>(g.items, kCtas);
   g.per_cta = (g.items + ctas - 1) / ctas;
   const dim3 grid((unsigned)((g.items + g.per_cta - 1) / g.per_cta));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return entry_cuda(a->dtype == BC_F32 ? launch_logits<float>(g, grid, st) : launch_logits<__nv_bfloat16>(g, grid, st),
+  return entry_cuda(f32 ? launch_logits<float>(g, grid, st) : launch_logits<__nv_bfloat16>(g, grid, st),
                     who);
 }

@@ -494,6 +494,41 @@ def test_logits_parts(kw, dtype):
     run_logits(4, 1501, dtype, seed=8, in_place=True, **kw)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V,at,pad,at_out,pad_out", [(1, 3, 1, 0, 0), (2, 1, 3, 1, 3), (7, 7, 6, 2, 1), (8, 5, 0, 5, 0),
+                                                     (9, 1, 8, 1, 0), (2047, 2, 1, 6, 3), (4095, 1, 1, 3, 7),
+                                                     (8185, 7, 5, 7, 5), (8192, 3, 1, 0, 0), (8193, 0, 2, 4, 1),
+                                                     (20001, 6, 1, 2, 2)])
+def test_logits_rows_anywhere(V, at, pad, at_out, pad_out, dtype):
+    """Rows that begin at any multiple of their type, other ones in than out,
+    and nothing written beside them."""
+    B, rng = 5, np.random.default_rng(V)
+    make = lambda off, stride: torch.full((off + B * stride + 16,), 77.0, dtype=dtype, device=DEV)
+    view = lambda buf, off, stride: buf[off:off + B * stride].view(B, stride)[:, :V]
+    src, dst = make(at, V + pad), make(at_out, V + pad_out)
+    x, out = view(src, at, V + pad), view(dst, at_out, V + pad_out)
+    x.copy_(torch.from_numpy(rng.standard_normal((B, V)).astype(np.float32)))
+    n = 40
+    kw = dict(hist=rng.integers(0, V, B * n), hist_start=np.arange(B + 1) * n, prompt_len=np.arange(B) * 9,
+              bias_ids=rng.integers(0, V, B * 6), bias_start=np.arange(B + 1) * 6,
+              mask=rng.integers(-2 ** 31, 2 ** 31, (B, -(-V // 32))))
+    kw = {k: v.astype(np.int32) for k, v in kw.items()}
+    kw.update(bias_vals=rng.standard_normal(B * 6).astype(np.float32), repetition=np.float32([1.3, 0.8, 1, 2, 0.5]),
+              frequency=np.float32([0.2, 0, -0.1, 0.3, 0.1]), presence=np.float32([0, 0.2, 0.1, -0.3, 0.4]))
+    want = og.logits_adjust(x.double().cpu().numpy(), **kw)
+    # as in run_logits: five f32 roundings of values below 2 |x| + 0.3 * 40 + 0.4 + |bias|, |x| and |bias| below 8
+    tol = 5 * 2.0 ** -24 * 40 + (np.abs(want) * 2.0 ** -8 if dtype == torch.bfloat16 else 0.0)
+    dev = {k: to(DEV, v) for k, v in kw.items()}
+    for o, buf, off, stride in ((out, dst, at_out, V + pad_out), (x, src, at, V + pad)):       # then in place
+        bc.logits_adjust(x, o, **dev)
+        got, ok = o.double().cpu().numpy(), np.isfinite(want)
+        np.testing.assert_array_equal(got[~ok], want[~ok])
+        assert (np.abs(got[ok] - want[ok]) <= np.broadcast_to(tol, want.shape)[ok]).all()
+        rest = torch.ones_like(buf, dtype=torch.bool)
+        view(rest, off, stride)[:] = False
+        assert (buf[rest] == 77).all()
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("code,dtype", [("e4m3", torch.bfloat16), ("int8", torch.float32)])
 @pytest.mark.parametrize("graph", [False, True])
