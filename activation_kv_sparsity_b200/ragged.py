@@ -275,7 +275,8 @@ class RaggedCache:
     step's plan (allocated with torch).  Per step: plan(delta), then per layer
     append(layer, k, v) and attend(layer, q, out).  Everything stays on the
     device, so a step can be captured into a graph.  Its methods share one
-    scratch: calls on several streams have to be ordered by the caller."""
+    scratch and its buffers are filled on the current stream when it is made:
+    calls on several streams have to be ordered by the caller."""
 
     def __init__(self, layers: int, batch: int, n_pages: int, n_kv_heads: int, group: int, head_dim: int,
                  max_blocks: int, max_tokens: int, max_q: int = 1, code: str = "e4m3", device="cuda"):
