@@ -147,7 +147,10 @@ __global__ void __launch_bounds__(kKv8Threads, kKv8Ctas) k_kv8_append(Kv8AppendA
       #pragma unroll
       for (int i = 0; i < NTOK; ++i) {
         const float4 x = raw[i].get();
-        code[i] = C::encode(__fmul_rn(x.x, inv), __fmul_rn(x.y, inv), __fmul_rn(x.z, inv), __fmul_rn(x.w, inv));
+        // zeros under a scale that is not a number, whatever x is: a code that
+        // is none would reach rows that mask the token
+        const uint32_t c = C::encode(__fmul_rn(x.x, inv), __fmul_rn(x.y, inv), __fmul_rn(x.z, inv), __fmul_rn(x.w, inv));
+        code[i] = inv > 0.f ? c : 0u;
       }
       auto again = [&](uint32_t w) {     // an earlier token's codes under the new scale
         const float4 y = kv8_decode4<TYPE>(w);

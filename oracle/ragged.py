@@ -158,10 +158,8 @@ def append(pool: np.ndarray, k: np.ndarray, v: np.ndarray, slots, kind: str) -> 
                     block[place[part][:off]] = encode(old * s_old * inv, kind)
                 if off == 0:
                     block[place[part]] = 0
-                with np.errstate(invalid="ignore"):
-                    scaled = new * inv
-                if np.isfinite(m):
-                    block[place[part][off:off + len(toks)]] = encode(scaled, kind)
+                scaled = new * inv if inv > 0 else np.zeros_like(new)
+                block[place[part][off:off + len(toks)]] = encode(scaled, kind)
                 at = 2 * PAGE * hd + 4 * part
                 block[at:at + 4] = np.array([s], f).view(np.uint8)
 

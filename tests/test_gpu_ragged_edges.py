@@ -1,0 +1,96 @@
+"""The ragged-batch operators on the GPU where numbers end: values that are
+not finite, weights and scales far apart, limits of lists and tables."""
+import numpy as np
+import pytest
+import torch
+
+import activation_kv_sparsity_b200 as bc
+from oracle import ragged as og
+from ragged_util import attention_tol, gen, make_pool, to
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+CODES = ["e4m3", "int8"]
+DTYPES = [torch.float32, torch.bfloat16]
+
+
+def ints(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=DEV)
+
+
+def attend(q, pool, lens, table, code, q_start=None, max_q=1, **kw):
+    """One call on host data: float64 [n_q][Hq][hd]."""
+    P, H, block = pool.shape
+    out = torch.full(q.shape, -77.0, dtype=q.dtype, device=DEV)
+    scratch = torch.zeros(bc.bc_kv8_attention_scratch_bytes(len(lens), H, q.shape[1] // H, max_q, q.shape[2]),
+                          dtype=torch.uint8, device=DEV)
+    bc.kv8_attention(q.to(DEV), to(DEV, pool), ints(lens), ints(table), out, scratch, code,
+                     q_start=None if q_start is None else ints(q_start), max_q=max_q, **kw)
+    assert bc.bc_kv8_attention_status(scratch.data_ptr(), None) == bc.BC_OK
+    return out.float().cpu().double().numpy()
+
+
+# ------------------------------------------------------------------ not finite
+def codes_of(pool, page, h, part, hd):
+    return pool[page, h][og._places(hd)[part]]
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hd", [64, 128])
+def test_append_of_a_value_that_is_not_finite_leaves_zeros(code, dtype, hd):
+    """The scale says it; a code that is not a number would reach rows that
+    mask the token."""
+    H = 2
+    pool = make_pool(3, H, hd, code, seed=1)
+    k = torch.randn(4, H, hd, generator=gen(2))
+    v = torch.randn(4, H, hd, generator=gen(3))
+    k[1, 1, 5], v[0, 0, 3], v[3, 1, hd - 1] = float("inf"), float("nan"), float("-inf")
+    k, v = k.to(dtype), v.to(dtype)
+    dev = to(DEV, pool)
+    # a fresh page, then a used one
+    for slots in ([16, 17, 18, 19], [2 * 16 + 5 + i for i in range(4)]):
+        og.append(pool, k.float().numpy(), v.float().numpy(), slots, code)
+        bc.kv8_append(k.to(DEV), v.to(DEV), ints(slots), dev, code)
+        got = dev.cpu().numpy()
+        np.testing.assert_array_equal(got[..., :32 * hd + 8], pool[..., :32 * hd + 8])
+        page, off = slots[0] // 16, slots[0] % 16
+        for part, h in ((0, 1), (1, 0), (1, 1)):
+            assert np.isnan(og.scale_of(got[page, h], part, hd))
+            assert (codes_of(got, page, h, part, hd)[off:off + 4] == 0).all()
+    # a finite token behind them: the scale stays, the code is 0
+    more = torch.full((1, H, hd), -3.0, dtype=dtype)
+    og.append(pool, more.float().numpy(), more.float().numpy(), [20], code)
+    bc.kv8_append(more.to(DEV), more.to(DEV), ints([20]), dev, code)
+    got = dev.cpu().numpy()
+    np.testing.assert_array_equal(got[..., :32 * hd + 8], pool[..., :32 * hd + 8])
+    assert (codes_of(got, 1, 0, 1, hd)[4] == 0).all() and (codes_of(got, 1, 0, 0, hd)[4] != 0).all()
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("part", [0, 1])
+def test_a_token_that_is_not_finite_stays_with_the_rows_that_see_its_block(code, dtype, hd, part):
+    """Drafts over the border of two pages: an infinity in the last token
+    reaches no earlier row of the page before; one that only the first row's
+    window holds reaches no later row."""
+    H, G, n, Q = 1, 2, 33, 8                              # queries at 25 .. 32
+    q = torch.randn(Q, H * G, hd, generator=gen(5)).to(dtype)
+    for bad, window in ((32, 0), (15, 11), (15, 12)):
+        kv = [torch.randn(n, H, hd, generator=gen(6 + i)).to(dtype) for i in range(2)]
+        kv[part][bad, 0, 7] = float("inf")
+        pool = np.zeros((3, H, og.block_bytes(hd)), np.uint8)
+        dev = to(DEV, pool)
+        for lo, hi in ((0, 32), (32, 33)):
+            bc.kv8_append(kv[0][lo:hi].to(DEV), kv[1][lo:hi].to(DEV), ints(range(lo, hi)), dev, code)
+        pool, table = dev.cpu().numpy(), np.array([[0, 1, 2]])
+        want = og.attention(q.float().numpy(), pool, [n], table, code, hd, [0, Q], Q, window=window)
+        got = attend(q, pool, [n], table, code, [0, Q], Q, window=window)
+        sees = np.array([(p >= bad) and (not window or 16 * (bad // 16) + 15 > p - window) for p in range(n - Q, n)])
+        assert sees.any() and not sees.all()
+        assert np.isnan(got[sees]).all()
+        fine = pool.copy()
+        fine[np.isnan(fine[:, :, 32 * hd:32 * hd + 8].copy().view(np.float32)).any(-1)] = 0
+        tol = attention_tol(want[~sees], q.double().numpy(), fine, code, hd, n, 0.0, None, dtype == torch.bfloat16)
+        assert (np.abs(got - want)[~sees] <= tol).all()
