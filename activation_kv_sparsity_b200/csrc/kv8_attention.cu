@@ -148,6 +148,9 @@ __device__ __forceinline__ float cap_logit(float x, float cap, float inv_cap) {
   return u < 0.01f ? p : fmaf(-2.f * cap, q, cap);
 }
 
+// the bytes of four e4m3 codes that are not numbers
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+
 // A segment as its flush and its masks need it.
 struct Segment {
   int h, begin, r0;          // kv head, first unit, the sequence's first query row
@@ -434,6 +437,38 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
       }
   };
 
+  // Value codes that are not numbers, on a page that not every row sees: a row
+  // that sees one becomes NaN in its dim, and the code 0, so that the rows that
+  // mask it get 0 times a number.  (The append writes no such code.)
+  auto take_out_nan = [&](uint8_t* blk, int pos0) {
+    #pragma unroll
+    for (int v = 0; v < V4; ++v) {
+      uint4* x = reinterpret_cast<uint4*>(blk + kPage * HD + (8 * v + g) * 64 + t * 16);
+      const uint4 y = *x;
+      const uint32_t n0 = nan_codes(y.x), n1 = nan_codes(y.y), n2 = nan_codes(y.z), n3 = nan_codes(y.w);
+      *x = make_uint4(y.x & ~n0, y.y & ~n1, y.z & ~n2, y.w & ~n3);
+      #pragma unroll 1
+      for (int r = 0; r < kA8Rows; ++r) {
+        const int at0 = __shfl_sync(0xffffffffu, at[0], r >> 1), at1 = __shfl_sync(0xffffffffu, at[1], r >> 1);
+        const int p = r & 1 ? at1 : at0;                  // the row's position
+        uint32_t sees = 0;
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int token = pos0 + 4 * t + j;
+          if (token <= p && (a.window == 0 || token > p - a.window)) sees |= 0xffu << (8 * j);
+        }
+        uint32_t hit = (n0 & sees ? 1u : 0u) | (n1 & sees ? 2u : 0u) | (n2 & sees ? 4u : 0u) | (n3 & sees ? 8u : 0u);
+        hit |= __shfl_xor_sync(0xffffffffu, hit, 1);
+        hit |= __shfl_xor_sync(0xffffffffu, hit, 2);
+        #pragma unroll
+        for (int d = 0; d < 4; ++d)
+          #pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (r == 2 * t + i && (hit >> d & 1u)) o[v][d >> 1][2 * (d & 1) + i] = __uint_as_float(0x7fc00000u);
+      }
+    }
+  };
+
   const float inv_cap = MODS && a.cap > 0.f ? 1.f / a.cap : 0.f;
   auto process = [&](uint8_t* blk, int lp) {
     const float* sc = reinterpret_cast<const float*>(blk + 2 * kPage * HD);
@@ -544,11 +579,15 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
       #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (pos0 + 4 * t + j < any_lo || pos0 + 4 * t + j > any_hi) keep &= ~(0xffu << (8 * j));
+      bool odd = false;
       #pragma unroll 1
       for (int v = 0; v < V4; ++v) {
         uint4* x = reinterpret_cast<uint4*>(blk + kPage * HD + (8 * v + g) * 64 + t * 16);
-        *x = make_uint4(x->x & keep, x->y & keep, x->z & keep, x->w & keep);
+        const uint4 y = make_uint4(x->x & keep, x->y & keep, x->z & keep, x->w & keep);
+        if (TYPE == BC_KV8_E4M3) odd |= (nan_codes(y.x) | nan_codes(y.y) | nan_codes(y.z) | nan_codes(y.w)) != 0;
+        *x = y;
       }
+      if (TYPE == BC_KV8_E4M3 && __any_sync(0xffffffffu, odd)) take_out_nan(blk, pos0);
       // these stores come before the next copy into this block
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }

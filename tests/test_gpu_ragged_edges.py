@@ -94,3 +94,36 @@ def test_a_token_that_is_not_finite_stays_with_the_rows_that_see_its_block(code,
         fine[np.isnan(fine[:, :, 32 * hd:32 * hd + 8].copy().view(np.float32)).any(-1)] = 0
         tol = attention_tol(want[~sees], q.double().numpy(), fine, code, hd, n, 0.0, None, dtype == torch.bfloat16)
         assert (np.abs(got - want)[~sees] <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("odd_scale", [None, 52, 31])
+def test_codes_that_are_not_numbers_stay_with_the_rows_that_see_them(dtype, hd, odd_scale):
+    """Whatever the bytes of a block are: a row that masks a token gets nothing
+    of it, a row that sees a value code that is not a number gets NaN in that
+    dim only, and everywhere from such a key or scale."""
+    H, G, n, Q = 2, 2, 61, 12                             # queries at 49 .. 60, of all tiles of 8 rows
+    q = torch.randn(Q, H * G, hd, generator=gen(15)).to(dtype)
+    kp, vp = og._places(hd)
+    pages = make_pool(4, H, hd, "e4m3", seed=16)
+    # (token, dim): seen by all rows, by the later ones, by the earlier ones in a window of 20, one of a later tile
+    spots = {"value": [(3, 1), (52, 2), (52, hd - 1), (33, 5), (60, 63), (31, 40)], "key": [(55, 9)]}
+    for part, window in (("value", 0), ("value", 20), ("value", 13), ("key", 0), ("key", 9)):
+        pool = pages.copy()
+        for i, (t, d) in enumerate(spots[part]):
+            h = i % 2
+            pool[t // 16, h][(vp if part == "value" else kp)[t % 16, d]] = 0x7F if i % 3 else 0xFF
+            if t == odd_scale:
+                at = 32 * hd + (4 if part == "value" else 0)
+                pool[t // 16, h, at:at + 4] = np.array([np.nan], np.float32).view(np.uint8)
+        table = np.array([[0, 1, 2, 3]])
+        want = og.attention(q.float().numpy(), pool, [n], table, "e4m3", hd, [0, Q], Q, window=window)
+        got = attend(q, pool, [n], table, "e4m3", [0, Q], Q, window=window)
+        np.testing.assert_array_equal(np.isnan(got), np.isnan(want), err_msg=f"{part} {window}")
+        # (every row sees token 52's page: all of it is NaN if a scale there is)
+        assert np.isnan(want).any() and (odd_scale == 52 or not np.isnan(want).all())
+        tol = attention_tol(np.nan_to_num(want), q.double().numpy(), pages, "e4m3", hd, n, 0.0, None,
+                            dtype == torch.bfloat16)
+        ok = ~np.isnan(want)
+        assert (np.abs(got - want)[ok] <= np.broadcast_to(tol, want.shape)[ok]).all()
