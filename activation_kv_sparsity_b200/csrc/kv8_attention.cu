@@ -34,14 +34,16 @@
 // would be 7/8 empty.  A row of q is scaled by a power of two so that its
 // largest element is in [1/2, 1).  A bf16 q is exact in f16 (down to 2^-24 of
 // its largest element), and weights of 11 bits serve a bf16 output of 8; for
-// f32 both are split in two f16 numbers, hi + lo (22 bits), for twice the
-// products.
+// f32 both are split in two f16 numbers, hi + lo (22 bits, or as many as the
+// smallest f16 number, 2^-24, leaves), for twice the products.
 // The key scale multiplies the logit.  The value scale v of a page enters the
-// weight, w = 2^(x + log2 v - mo + 4), with a second reference mo for x +
+// weight, w = 2^(x + log2 v - mo + lift), with a second reference mo for x +
 // log2 v: the f16 weight is then relative to the largest weight times scale
 // seen, however far apart the scales are.  The references m and mo follow
-// the maxima only when one is passed by more than 2^8 (one vote a page): the
-// reductions over the lanes and the rescaling of o leave the usual path.
+// the maxima only when one is passed by more than 2^slack (one vote a page): the
+// reductions over the lanes and the rescaling of o leave the usual path.  With
+// slack 2 (f32) they do so a little more often than with 8, 0.2 us of 52.7 for
+// four sequences of 16K to 128K tokens at half the pages.
 //
 // Fragment order.  Lane (g, t) = (lane / 4, lane % 4).  Dims are contracted
 // in the order in which a lane finds them, 64u + 16t + 4w + 0..3 for step
@@ -160,7 +162,15 @@ struct Segment {
 
 // References below every logit: nothing seen yet.
 constexpr float kNoMax = -1e38f;
-constexpr float kSlack = 8.f, kLift = 4.f;   // w <= 2^(kSlack + kLift), within f16
+// A weight is at most 2^(slack + lift) = 2^15, within f16, and the largest at
+// least 2^lift.  Half the smallest f16 number, 2^-25, is the error of a small one:
+// 2^-32 of the largest under bf16 outputs, 2^-38 under f32 ones, whose references
+// follow sooner for it.  The denominator sums weights of 32 bits, so that what
+// lies below is lost from the output.
+template <bool SPLIT>
+struct Refs {
+  static constexpr float slack = SPLIT ? 2.f : 8.f, lift = 15.f - slack;
+};
 
 // What a sequence needs of the cache.
 struct Seq {
@@ -196,6 +206,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   constexpr int BLK = kv8_block_bytes(HD);
   constexpr int U = HD / 64, V4 = HD / 32;
   constexpr int SROW = HD + 4;             // a partial's row: o, then m, l, mo
+  constexpr float kSlack = Refs<SPLIT>::slack, kLift = Refs<SPLIT>::lift;
   const bc_kv8_attention_args& a = ga.a;
   const int B = a.batch, H = a.n_kv_heads, G = a.group;
 
@@ -617,9 +628,13 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     }
   };
 
-  // out = o / l 2^(mo - m - kLift); nothing seen: 0
+  // out = (o 2^-kLift / l) 2^(mo - m), two factors since one alone could fall
+  // below the normal numbers; nothing seen: 0
   auto final_factor = [](float mm, float ll, float mmo) {
-    return ll == 0.f ? 0.f : exp2f(mmo - mm - kLift) / ll;
+    return ll == 0.f ? make_float2(0.f, 0.f) : make_float2(exp2f(-kLift) / ll, exp2f(mmo - mm));
+  };
+  auto times = [](float4 y, float2 f) {
+    return make_float4(y.x * f.x * f.y, y.y * f.x * f.y, y.z * f.x * f.y, y.w * f.x * f.y);
   };
   auto put = [&](int row, int j, int d, float4 y) {       // 4 dims of query row `row`, head j
     const size_t e = ((size_t)row * H * G + j) * HD + d;
@@ -641,7 +656,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
       ll += __shfl_xor_sync(0xffffffffu, ll, 16);
       if (gave_up >= 0) ll = __uint_as_float(0x7fc00000u);
       const int in = 2 * t + i, row = s.row0 + in;
-      const float f = final_factor(m[i], ll, mo[i]);
+      const float2 f = final_factor(m[i], ll, mo[i]);
       const int query = query_of(row), src = s.r0 + query;
       const bool ok = row < s.rows && src >= 0 && src < a.n_q;
       #pragma unroll
@@ -649,7 +664,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
         const float4 y = make_float4(o[v][0][i], o[v][0][2 + i], o[v][1][i], o[v][1][2 + i]);
         const int d = 4 * (8 * v + g);
         if (dst) *reinterpret_cast<float4*>(dst + in * SROW + d) = y;
-        else if (ok) put(src, (s.h - query) * G + row, d, make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
+        else if (ok) put(src, (s.h - query) * G + row, d, times(y, f));
       }
       if (dst && g == 0) {
         float* ml = dst + in * SROW + HD;
@@ -788,9 +803,9 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     }
     if (c.s0 >= c0 && c.s1 <= c1) {
       const int of_seq = c.row0 + row, query = query_of(of_seq), src = s_row[c.b] + query;
-      const float f = final_factor(M, L, MO);
+      const float2 f = final_factor(M, L, MO);
       if (src >= 0 && src < a.n_q)
-        put(src, (c.h - query) * G + of_seq, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+        put(src, (c.h - query) * G + of_seq, d, times(acc, f));
     } else {
       float* dst = ga.part + ((blockIdx.x * 2 + (c.s0 < c0 ? 0 : 1)) * kA8Rows + row) * SROW;
       *reinterpret_cast<float4*>(dst + d) = acc;
@@ -816,7 +831,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
   __syncthreads();
   if (!s_last[0] && !s_last[1]) return;
   float* s_fac = reinterpret_cast<float*>(ring);        // [2][kA8Rows][partials]
-  float* s_out = s_fac + 2 * kA8Rows * kA8MaxCtas;      // [2][kA8Rows]
+  float2* s_out = reinterpret_cast<float2*>(s_fac + 2 * kA8Rows * kA8MaxCtas);      // [2][kA8Rows]
   // partial of row `row` in the x-th CTA of segment c, which begins in the first one
   auto partial = [&](const Cut& c, int x, int row) {
     return ga.part + (((c.cta0 + x) * 2 + (x == 0 ? 1 : 0)) * kA8Rows + row) * SROW;
@@ -873,9 +888,9 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
       }
     }
     const int of_seq = c.row0 + row, query = query_of(of_seq), src = s_row[c.b] + query;
-    const float f = s_out[ir];
+    const float2 f = s_out[ir];
     if (src >= 0 && src < a.n_q)
-      put(src, (c.h - query) * G + of_seq, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+      put(src, (c.h - query) * G + of_seq, d, times(acc, f));
   }
 }
 

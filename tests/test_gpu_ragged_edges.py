@@ -127,3 +127,64 @@ def test_codes_that_are_not_numbers_stay_with_the_rows_that_see_them(dtype, hd, 
                             dtype == torch.bfloat16)
         ok = ~np.isnan(want)
         assert (np.abs(got - want)[ok] <= np.broadcast_to(tol, want.shape)[ok]).all()
+
+
+# ------------------------------------------------------------------ far apart
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("at", [0, 60 * 16 + 5])
+def test_many_small_weights_beside_a_large_one(code, dtype, at):
+    """One token outweighs each of the others by 2^D and has the value 0, so
+    that the output is what the others add up to.
+
+    Relative to the output: the logits (base 2, up to 30) have five f32
+    roundings, the exponents of the value scales (up to 40) three of 2^-24 of
+    themselves, exponentials and the two-part weight 2^-21; 125 pages are summed
+    one after the other, each with an error of 2^-23 of the sum, in numerator
+    and denominator.  Besides, a weight has an absolute floor, half the smallest
+    f16 number, under a largest one of at least 2^13 (2^7 with bf16 outputs,
+    whose weights have one part, 2^-11, and are rounded to 2^-8).
+
+    222 sequences of 8 heads: on 148 SMs each is the work of one warp."""
+    B, H, hd, n = 222, 8, 64, 2000
+    half = dtype == torch.bfloat16
+    g = gen(21)
+    k, v = torch.zeros(n, 1, hd), 0.5 + 0.5 * torch.rand(n, 1, hd, generator=g)
+    k[at, 0, 0], v[at] = 1.0, 0.0
+    n_pages = og.pages_of(n)
+    one = np.zeros((n_pages, 1, og.block_bytes(hd)), np.uint8)
+    og.append(one, k.numpy(), v.numpy(), np.arange(n), code)
+    pool = np.repeat(one, H, axis=1)
+    table = np.arange(n_pages)[None].repeat(B, 0)
+    q = torch.zeros(1, 1, hd)
+    q[0, 0, 0] = 1.0
+    for D in (10.0, 17.5, 20.3, 23.7, 26.2, 29.8):
+        scale = float(np.float32(D * np.log(2.0)))
+        want = og.attention(q.numpy(), one, [n], table[:1], code, hd, scale=scale)
+        got = attend(q.to(dtype).expand(B, H, hd).contiguous(), pool, [n] * B, table, code, scale=scale)
+        rel = (5 * 30 + 3 * 40) * 2.0 ** -24 + 2.0 ** -21 + 2 * 125 * 2.0 ** -23
+        tol = np.abs(want) * (rel + (2.0 ** -8 + 2.0 ** -11 if half else 0.0)) + n * 2.0 ** (-32 if half else -38)
+        assert (np.abs(got - want) <= tol).all(), (D, float((np.abs(got - want) / np.abs(want)).max()))
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("n", [64, 3000])
+def test_values_at_the_end_of_the_normal_numbers(code, n):
+    """Value scales of 2^-126.  Relative to the output: exponents of up to 140
+    have three roundings of 2^-24 of themselves, weights and exponentials
+    2^-20, the sums (n / 16 + 32) 2^-23; the logits (base 2, up to 10) five
+    roundings; and an output rounds to a multiple of 2^-149, twice."""
+    H, G, hd = 2, 2, 64
+    g = gen(31)
+    k = 0.3 * torch.randn(n, H, hd, generator=g)
+    v = 1e-37 * (0.5 + 0.5 * torch.rand(n, H, hd, generator=g))
+    n_pages = og.pages_of(n)
+    pool = np.zeros((n_pages, H, og.block_bytes(hd)), np.uint8)
+    og.append(pool, k.numpy(), v.numpy(), np.arange(n), code)
+    q = 0.5 * torch.randn(1, H * G, hd, generator=g)
+    table = np.arange(n_pages)[None]
+    want = og.attention(q.numpy(), pool, [n], table, code, hd)
+    got = attend(q, pool, [n], table, code)
+    rel = 3 * 140 * 2.0 ** -24 + 2.0 ** -20 + 2 * (n / 16 + 32) * 2.0 ** -23 + 2 * 5 * 10 * 2.0 ** -24
+    assert (want > 2.0 ** -126).all()
+    assert (np.abs(got - want) <= want * rel + 2.0 ** -148).all(), float((np.abs(got - want) / want).max())
