@@ -32,10 +32,10 @@
 // in f16), the cache as the A operand and the 8 rows as its 8 columns, so no
 // part of a tile is idle: S^T = K Q^T, then O^T = V^T P^T.  A tcgen05 tile
 // would be 7/8 empty.  A row of q is scaled by a power of two so that its
-// largest element is in [1/2, 1).  A bf16 q is exact in f16 (down to 2^-24 of
-// its largest element), and weights of 11 bits serve a bf16 output of 8; for
-// f32 both are split in two f16 numbers, hi + lo (22 bits, or as many as the
-// smallest f16 number, 2^-24, leaves), for twice the products.
+// largest element is in [2^14, 2^15).  A bf16 q is exact in f16 (elements below
+// 2^-31 of the largest: to 2^-39 of it), and weights of 11 bits serve a bf16
+// output of 8; for f32 both are split in two f16 numbers, hi + lo (22 bits, or
+// as many as the smallest f16 number, 2^-24, leaves), for twice the products.
 // The key scale multiplies the logit.  The value scale v of a page enters the
 // weight, w = 2^(x + log2 v - mo + lift), with a second reference mo for x +
 // log2 v: the f16 weight is then relative to the largest weight times scale
@@ -433,9 +433,9 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
     for (int d = 0; d < 16 * U; ++d) top = max(top, __float_as_uint(x[d]) & 0x7fffffffu);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const int e = (int)(top >> 23);                    // q 2^(126 - e) is below 1
-    const float f = e == 255 ? __uint_as_float(0x7fc00000u) : ldexpf(1.f, 126 - e);
-    const float back = ldexpf(MODS ? a.scale : a.scale * kLog2e, e - 126);
+    const int e = max((int)(top >> 23), 14);           // q 2^(141 - e) is below 2^15
+    const float f = e == 255 ? __uint_as_float(0x7fc00000u) : ldexpf(1.f, 141 - e);
+    const float back = ldexpf(MODS ? a.scale : a.scale * kLog2e, e - 141);
     qs[0] = __shfl_sync(0xffffffffu, back, 8 * t);
     qs[1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     #pragma unroll

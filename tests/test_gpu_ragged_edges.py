@@ -188,3 +188,28 @@ def test_values_at_the_end_of_the_normal_numbers(code, n):
     rel = 3 * 140 * 2.0 ** -24 + 2.0 ** -20 + 2 * (n / 16 + 32) * 2.0 ** -23 + 2 * 5 * 10 * 2.0 ** -24
     assert (want > 2.0 ** -126).all()
     assert (np.abs(got - want) <= want * rel + 2.0 ** -148).all(), float((np.abs(got - want) / want).max())
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dtype,top", [(torch.float32, 2.0 ** 15), (torch.float32, 2.0 ** 22),
+                                       (torch.bfloat16, 2.0 ** 20)])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_a_query_channel_that_outweighs_the_others(code, dtype, top, hd):
+    """A channel of q far above the others, where the keys are 0: the logits
+    come from the others, which the tolerance is taken from."""
+    H, G, n = 2, 4, 200
+    g = gen(41)
+    k, v = torch.randn(n, H, hd, generator=g), torch.randn(n, H, hd, generator=g)
+    k[..., 9] = 0.0
+    n_pages = og.pages_of(n)
+    pool = np.zeros((n_pages, H, og.block_bytes(hd)), np.uint8)
+    og.append(pool, k.numpy(), v.numpy(), np.arange(n), code)
+    q = torch.randn(1, H * G, hd, generator=g).to(dtype)
+    q[..., 9] = top
+    table = np.arange(n_pages)[None]
+    want = og.attention(q.float().numpy(), pool, [n], table, code, hd)
+    got = attend(q, pool, [n], table, code)
+    rest = q.double().numpy()
+    rest[..., 9] = 0.0
+    tol = attention_tol(want, rest, pool, code, hd, n, 0.0, None, dtype == torch.bfloat16)
+    assert (np.abs(got - want) <= tol).all(), float(np.abs(got - want).max())
