@@ -213,3 +213,24 @@ def test_a_query_channel_that_outweighs_the_others(code, dtype, top, hd):
     rest[..., 9] = 0.0
     tol = attention_tol(want, rest, pool, code, hd, n, 0.0, None, dtype == torch.bfloat16)
     assert (np.abs(got - want) <= tol).all(), float(np.abs(got - want).max())
+
+
+@pytest.mark.parametrize("code", CODES)
+def test_long_sums_are_not_biased(code):
+    """65536 equal weights of values of one sign, all pages of a head in one
+    warp (as above), f32.  Relative to the output: log2 of a value scale
+    (2^-8.8) is off by 2^-22 of itself, the exponents (up to 16) have three
+    roundings, weights and exponentials 2^-20; and of 4096 additions rounded to
+    nearest, each off by 0.29 units of 2^-23 in the root mean square, six
+    standard deviations.  (Sums cut off instead would be low by up to 4096
+    2^-24, 2.4e-4.)"""
+    B, H, hd, P, n_pages = 222, 8, 64, 64, 4096
+    g = gen(51)
+    v = 0.5 + 0.5 * torch.rand(P * 16, 1, hd, generator=g)
+    one = np.zeros((P, 1, og.block_bytes(hd)), np.uint8)
+    og.append(one, np.zeros(v.shape, np.float32), v.numpy(), np.arange(P * 16), code)
+    want = og.read(one, np.arange(P * 16), code, hd)[1].mean(0)
+    got = attend(torch.randn(B, H, hd, generator=g), np.repeat(one, H, axis=1), [16 * n_pages] * B,
+                 (np.arange(n_pages) % P)[None].repeat(B, 0), code)
+    rel = np.log(2.0) * (9 * 2.0 ** -22 + 3 * 16 * 2.0 ** -24) + 2.0 ** -20 + 6 * 0.29 * 4096 ** 0.5 * 2.0 ** -23
+    assert (np.abs(got / want - 1) <= rel).all(), (float(np.abs(got / want - 1).max()), rel)
