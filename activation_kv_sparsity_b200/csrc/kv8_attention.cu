@@ -98,11 +98,6 @@ __device__ __forceinline__ float lg2(float x) {          // scales are 0, NaN or
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float min_nan(float x, float y) {       // not a number if either is not
-  float z;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
-  return z;
-}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -562,18 +557,27 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
           o[v][i][3] *= ao[1];
         }
     }
-    float w[2][2];
+    // A scale that is not a number makes even a weight of 0 one.
+    float w[2][2], z[2];
     #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      // the bound keeps 0 * f a 0; it is passed only where p is below 2^-96.  A
-      // scale that is not a number makes even a weight of 0 one.
-      const float f = ex2(min_nan(lvs + (m[i] - mo[i]) + kLift, 100.f));
+      z[i] = lvs + (m[i] - mo[i]) + kLift;
+      const float f = ex2(z[i]);
       #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float p = ex2(y[i][j]);
         l[i] += p;
         w[i][j] = p * f;
       }
+    }
+    // A factor near or past the largest number, of values that make up for
+    // logits far below the row's others: the weight from one exponent.  (Up to
+    // 2^96 a p that is cut to 0 stands for less than f16 holds.)
+    if (__any_sync(0xffffffffu, fmaxf(z[0], z[1]) > 96.f)) {
+      #pragma unroll
+      for (int i = 0; i < 2; ++i)
+        #pragma unroll
+        for (int j = 0; j < 2; ++j) w[i][j] = ex2(y[i][j] + z[i]);
     }
     if (!whole) {
       // masked tokens weigh nothing, whatever the scales are (a key scale

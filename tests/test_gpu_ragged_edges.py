@@ -234,3 +234,33 @@ def test_long_sums_are_not_biased(code):
                  (np.arange(n_pages) % P)[None].repeat(B, 0), code)
     rel = np.log(2.0) * (9 * 2.0 ** -22 + 3 * 16 * 2.0 ** -24) + 2.0 ** -20 + 6 * 0.29 * 4096 ** 0.5 * 2.0 ** -23
     assert (np.abs(got / want - 1) <= rel).all(), (float(np.abs(got / want - 1).max()), rel)
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("swap", [False, True])
+def test_value_scales_that_outweigh_the_logits(code, dtype, swap):
+    """A page with logit 0 (base 2) and small values, another with logit -D and
+    values that make up for it, however far apart both are.  Relative to the
+    output: the logits (up to 140) have five roundings, the exponents (up to
+    150) four, log2 of a value scale (up to 115) is off by 2^-22 of itself,
+    weights and exponentials 2^-20, the output and its bf16 weights as ever.
+    Sequences so many that a warp reads both pages of some."""
+    B, hd = 2000, 64
+    q = torch.zeros(B, 1, hd, dtype=dtype)
+    q[:, 0, 0] = 1.0
+    for D, low, high in ((95, -100, 0), (97, -97, 3), (130, -75, 58), (110, -60, 50), (138, -100, 45), (60, -60, 1),
+                         (100, -105, 10)):
+        k, v = torch.zeros(32, 1, hd), torch.ones(32, 1, hd)
+        k[16:, 0, 0] = -1.0
+        v[:16] *= 2.0 ** low
+        v[16:] *= 2.0 ** high
+        pool = np.zeros((2, 1, og.block_bytes(hd)), np.uint8)
+        og.append(pool, k.numpy(), v.numpy(), np.arange(32), code)
+        pages = [[1, 0] if swap else [0, 1]]
+        scale = float(np.float32(D * np.log(2.0)))
+        want = og.attention(q[:1].float().numpy(), pool, [32], np.array(pages), code, hd, scale=scale)
+        got = attend(q, pool, [32] * B, pages * B, code, scale=scale)
+        rel = np.log(2.0) * ((5 * 140 + 4 * 150) * 2.0 ** -24 + 115 * 2.0 ** -22) + 2.0 ** -20
+        rel += 2.0 ** -8 + 2.0 ** -11 if dtype == torch.bfloat16 else 2.0 ** -24
+        assert (np.abs(got / want - 1) <= rel).all(), (D, low, high, float((got / want).min()))
