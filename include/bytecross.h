@@ -574,7 +574,9 @@ BC_API bc_status bc_kv8_attention_status(void* scratch, void* stream);
  *     history from its prompt_len[b]-th token on;
  *   x + the bias listed for v (of an id listed twice, the last);
  *   -inf if the row has a mask and v's bit in it is 0.
- * Arithmetic in f32, rounded once to the output's type.
+ * Arithmetic in f32, rounded once to the output's type.  x / repetition is a
+ * product with the rounded reciprocal: a penalty whose reciprocal is infinite
+ * (below 2^-128) gives infinite logits.
  *   logits, out  f32 or bf16 [batch] rows of vocab, strides in elements; out
  *                may be logits (with the same stride), else they do not overlap
  *   hist         token ids; row b's are hist[hist_start[b] .. hist_start[b + 1]),

@@ -264,3 +264,30 @@ def test_value_scales_that_outweigh_the_logits(code, dtype, swap):
         rel = np.log(2.0) * ((5 * 140 + 4 * 150) * 2.0 ** -24 + 115 * 2.0 ** -22) + 2.0 ** -20
         rel += 2.0 ** -8 + 2.0 ** -11 if dtype == torch.bfloat16 else 2.0 ** -24
         assert (np.abs(got / want - 1) <= rel).all(), (D, low, high, float((got / want).min()))
+
+
+# ------------------------------------------------------------------ logits
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_repetition_over_its_range(dtype):
+    """Penalties from the smallest normal number to the largest.  x / r as a
+    product with the reciprocal: two roundings of 2^-24, a reciprocal that is not
+    normal itself (of r above 2^126) to half a step of 2^-149, which is 2^-22 of
+    it, one step of a result that is not normal, then the output's."""
+    reps = np.array([2.0 ** -126, 1.2e-38, 3e-20, 0.7, 1.3, 5e30, 2.0 ** 126, 1e38, 2e38, 3.4e38, -2e38], np.float32)
+    x = np.array([1e-3, 2e-6, 3e-30, 5.0, 3e38, -3.0, -2e-3, 0.0, 2e-38], np.float32)
+    B, V = len(reps), len(x)
+    lg = torch.from_numpy(np.tile(x, (B, 1))).to(dtype)
+    hist = np.tile(np.arange(V), B).astype(np.int32)
+    start = (np.arange(B + 1) * V).astype(np.int32)
+    a, r = lg.double().numpy(), reps.astype(np.float64)[:, None]
+    want = np.where(a > 0, a / r, a * r)
+    assert not ((np.abs(want) > 3.35e38) & (np.abs(want) < 3.42e38)).any()       # none at the border of infinity
+    out = torch.empty_like(lg, device=DEV)
+    bc.logits_adjust(lg.to(DEV), out, hist=to(DEV, hist), hist_start=to(DEV, start), repetition=to(DEV, reps))
+    got = out.cpu().double().numpy()
+    over = np.abs(want) > 3.4e38
+    assert (np.isinf(got) == over).all() and (np.sign(got) == np.sign(want))[over].all()
+    half = dtype == torch.bfloat16
+    rel = 2 * 2.0 ** -24 + (np.abs(r) > 2.0 ** 126) * 2.0 ** -22 + (2.0 ** -8 if half else 0.0)
+    tol = np.abs(want) * rel + 2.0 ** -149 + (2.0 ** -134 if half else 0.0)
+    assert (np.abs(got - want) <= tol)[~over].all()
