@@ -291,3 +291,32 @@ def test_repetition_over_its_range(dtype):
     rel = 2 * 2.0 ** -24 + (np.abs(r) > 2.0 ** 126) * 2.0 ** -22 + (2.0 ** -8 if half else 0.0)
     tol = np.abs(want) * rel + 2.0 ** -149 + (2.0 ** -134 if half else 0.0)
     assert (np.abs(got - want) <= tol)[~over].all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hist,bias", [(8192, 0), (8191, 2), (8188, 4), (8187, 4), (8187, 9), (8189, 6), (8193, 2),
+                                       (4000, 5000), (4001, 4192), (0, 8192), (0, 8195)])
+def test_logits_lists_at_the_limit_of_shared_memory(hist, bias, dtype):
+    """8192 entries of a row's lists, the history padded to a multiple of 4 and
+    then the biases, lie in shared memory; lists that fill it exactly, and cuts
+    through either.  Every bias id comes twice, the first and the last entry
+    among them, so that some pairs have one on each side of a cut."""
+    V, B, g = 20000, 2, gen(hist + bias)
+    x = torch.randn(B, V, generator=g).to(dtype)
+    h = torch.randint(0, V, (hist,), generator=g).int()
+    h[:hist // 3] = h[hist // 3:hist // 3 * 2]                  # ids of the prompt that come up again
+    half_b = torch.randperm(V, generator=g)[:(bias + 1) // 2].int()
+    ids = torch.cat([half_b, half_b])[:bias].repeat(B)
+    kw = dict(repetition=np.float32([1.3, 0.8]), frequency=np.float32([0.2, -0.1]), presence=np.float32([0.1, 0.4]))
+    if hist:
+        kw.update(hist=h.repeat(B).numpy(), hist_start=np.arange(B + 1, dtype=np.int32) * hist,
+                  prompt_len=np.array([hist // 3, 5], np.int32))
+    if bias:
+        kw.update(bias_ids=ids.numpy(), bias_vals=torch.randn(B * bias, generator=g).numpy(),
+                  bias_start=np.arange(B + 1, dtype=np.int32) * bias)
+    want = og.logits_adjust(x.double().numpy(), **kw)
+    out = torch.full((B, V), 77.0, dtype=dtype, device=DEV)
+    bc.logits_adjust(x.to(DEV), out, **{k: to(DEV, v) for k, v in kw.items()})
+    # five f32 roundings of values below 2 |x| + 0.2 c + 0.4 + |bias| < 20, then the output's
+    tol = 5 * 2.0 ** -24 * 20 + (np.abs(want) * 2.0 ** -8 if dtype == torch.bfloat16 else 0.0)
+    assert (np.abs(out.cpu().double().numpy() - want) <= tol).all()
