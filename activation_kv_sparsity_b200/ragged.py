@@ -297,7 +297,10 @@ class RaggedCache:
 
     def plan(self, delta, stream=None):
         """delta int32 [batch]: tokens each sequence takes (or, negative,
-        drops); updates lens, table, free_list, q_start, slots, positions."""
+        drops); updates lens, table, free_list, q_start, slots, positions.  A
+        dropped token's effect on the scales of a page that other tokens of
+        its sequence keep stays: a rejected draft with an outlier leaves coarser
+        codes there, one that is not finite NaN."""
         block_tables(self.lens, delta, self.table, self.free_list, self.n_free, self.lens, self.n_free, self.q_start,
                      self.slots, self.positions, self.ticket, stream)
 

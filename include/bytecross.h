@@ -489,6 +489,8 @@ BC_API bc_status bc_block_tables(const bc_block_tables_args* a, void* stream);
  * zero.  If a new key (value) is infinite or NaN, the block's key (value)
  * scale becomes NaN, its new codes 0, and every attention row that sees the
  * block NaN.
+ * Tokens that are dropped later (a rejected draft) keep their effect on the
+ * block's scale, NaN included, until the page's token 0 is written again.
  * Errors: BC_EINVAL, BC_ECUDA. */
 BC_API bc_status bc_kv8_append(const void* k, const void* v, bc_dtype dtype, long long k_stride, long long v_stride,
                                const int* slots, int n_tokens, void* pool, bc_kv8_type type, int n_pages,

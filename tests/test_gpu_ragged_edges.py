@@ -320,3 +320,43 @@ def test_logits_lists_at_the_limit_of_shared_memory(hist, bias, dtype):
     # five f32 roundings of values below 2 |x| + 0.2 c + 0.4 + |bias| < 20, then the output's
     tol = 5 * 2.0 ** -24 * 20 + (np.abs(want) * 2.0 ** -8 if dtype == torch.bfloat16 else 0.0)
     assert (np.abs(out.cpu().double().numpy() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("code", CODES)
+def test_dropped_tokens_keep_their_mark_on_the_scale(code):
+    """As the definition has it: tokens taken back leave the page's scale, an
+    outlier's or one that is not a number, until its token 0 is written again;
+    pages given back and pages before are not touched."""
+    H, hd = 1, 64
+    cache = bc.RaggedCache(1, 1, 4, H, 1, hd, 4, 64, max_q=4, code=code, device=DEV)
+    g = gen(61)
+    x = lambda n, f=1.0: f * torch.randn(n, H, hd, generator=g).clamp(-3, 3)
+    scale = lambda page: float(og.scale_of(cache.pool[0, page, 0].cpu().numpy(), 1, hd))
+    pages = []
+
+    def step(delta, v):
+        cache.plan(ints([delta]))
+        if v is not None:
+            cache.append(0, v.to(DEV), v.to(DEV))
+        pages[:] = cache.table[0].cpu().tolist()
+    step(20, x(20))
+    first, second = scale(pages[0]), scale(pages[1])
+    step(4, torch.cat([x(3), x(1, 1000.0)]))               # a draft with an outlier, rejected
+    coarse = scale(pages[1])
+    assert coarse > 100 * second
+    step(-4, None)
+    step(2, x(2))
+    assert scale(pages[1]) == coarse and scale(pages[0]) == first
+    step(3, torch.full((3, H, hd), float("inf")))          # one that is not finite
+    step(-3, None)
+    q, out = torch.randn(1, 1, hd, generator=g).to(DEV), torch.empty(1, 1, hd, device=DEV)
+    step(1, x(1))
+    cache.attend(0, q, out)
+    assert torch.isnan(out).all() and np.isnan(scale(pages[1]))
+    cache.attend(0, q, out, pages=ints([[[0]]]), n_sel=ints([1]))
+    assert torch.isfinite(out).all()                       # the page before
+    step(-8, None)                                         # 15 tokens: the page is given back
+    step(3, x(3))
+    cache.attend(0, q, out)
+    assert torch.isfinite(out).all() and np.isfinite(scale(pages[1])) and scale(pages[0]) >= first
+    cache.status()
