@@ -120,7 +120,9 @@ __global__ void __launch_bounds__(NT) k_block_tables(const __grid_constant__ bc_
     if (at > a.max_tokens) cand[i] = 0;
     need[i] = cand[i] ? pages_of(len[i] + cand[i]) - pages_of(len[i]) : 0;
     mine.a += need[i];
-    if (b < B) s_back[b] = (int)min(rel, (long long)a.n_pages + 1);
+    // (exact for the sequences that the list has room for: rooms and a
+    // sequence's pages are at most 2^27)
+    if (b < B) s_back[b] = (int)min(rel, (long long)INT32_MAX);
     rel += back[i];
   }
   const Sum2 s2 = block_scan2<NT>(mine, red, &total);
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(NT) k_block_tables(const __grid_constant__ bc_
   if (threadIdx.x == 0) {
     s_start[B] = n_tok;
     s_take[B] = n_take;
-    s_back[B] = (int)min(n_back, (long long)a.n_pages + 1);
+    s_back[B] = (int)min(n_back, (long long)INT32_MAX);
     if (blockIdx.x == 0) a.q_start[B] = n_tok;
   }
   __syncthreads();

@@ -430,8 +430,9 @@ BC_API size_t bc_kv8_pool_bytes(int n_pages, int n_kv_heads, int head_dim);
  *   > 0  it takes delta new tokens and the pages they need;
  *   0    nothing.
  * The free pages are free_list[0 .. n_free) followed by the pages given back
- * in this call (in order of sequence, then of page); pages are taken from the
- * end of that list, in order of sequence.  A sequence that asks for tokens is
+ * in this call (in order of sequence, then of page), cut at n_pages (which takes
+ * a table that names a page twice); pages are taken from the end of that list, in
+ * order of sequence.  A sequence that asks for tokens is
  * refused, and keeps its length, if
  *   lens + delta > 16 max_blocks, or
  *   the delta of the sequences up to it (those refused so far by the line

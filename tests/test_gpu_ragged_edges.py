@@ -360,3 +360,27 @@ def test_dropped_tokens_keep_their_mark_on_the_scale(code):
     cache.attend(0, q, out)
     assert torch.isfinite(out).all() and np.isfinite(scale(pages[1])) and scale(pages[0]) >= first
     cache.status()
+
+
+# ------------------------------------------------------------------ the plan
+@pytest.mark.parametrize("B", [1, 3, 200])
+def test_plan_that_is_given_back_more_pages_than_there_are(B):
+    """Tables that name pages twice: the list of free pages is cut at n_pages,
+    and what is in it comes from the right places."""
+    rng = np.random.default_rng(B)
+    max_blocks, n_pages, n_free, max_tokens = 12, 7, 2, 40
+    table = rng.integers(0, n_pages, (B, max_blocks)).astype(np.int32)
+    free = rng.permutation(n_pages).astype(np.int32)
+    lens = rng.integers(16 * 9, 16 * max_blocks + 1, B).astype(np.int32)
+    delta = np.full(B, -2 ** 31, np.int64)
+    if B > 1:
+        delta[1], lens[1], delta[2] = 33, 17, -70
+    want = og.block_tables(lens, delta, table, free, n_free, max_tokens)
+    d = dict(lens=ints(lens), delta=ints(delta), table=ints(table), free_list=ints(free), n_free=ints([n_free]),
+             lens_out=ints([-7] * B), n_free_out=ints([-7]), q_start=ints([-7] * (B + 1)),
+             slots=ints([-7] * max_tokens), positions=ints([-7] * max_tokens), ticket=ints([0]))
+    bc.block_tables(**d)
+    for name, got in (("table", d["table"]), ("free_list", d["free_list"]), ("n_free", d["n_free_out"]),
+                      ("lens", d["lens_out"]), ("q_start", d["q_start"]), ("slots", d["slots"]),
+                      ("positions", d["positions"])):
+        np.testing.assert_array_equal(got.cpu().numpy(), np.reshape(want[name], got.shape), err_msg=name)
