@@ -315,7 +315,9 @@ class RaggedCache:
 
     def attend(self, layer: int, q, out, stream=None, **options):
         """q [n_q][Hq][hd], the queries of the step's new tokens; options as
-        for kv8_attention."""
+        for kv8_attention.  Of a sequence with more than max_q of them (a prompt)
+        only the first max_q rows of out are written, as kv8_attention has it;
+        rows behind the plan's last token may pad q."""
         kv8_attention(q, self._pools[layer], self.lens, self.table, out, self.scratch, self.code, self.q_start,
                       self.max_q, stream=stream, **options)
 
