@@ -202,6 +202,8 @@ def kv8_attention(q, pool, lens, table, out, scratch, code="e4m3", q_start=None,
             raise ValueError(f"{who}: pages must be [batch][n_kv_heads][max_sel], max_sel at least 1")
         max_sel = pages.shape[2]
     _fits(who, n_q, B, max_blocks, max_sel, max_q, window)
+    if cap and abs(cap) < 2.0 ** -126:                    # in 32 bits some of these are 0, which means none
+        raise ValueError(f"{who}: cap must be 0 or a positive normal number, not {cap}")
     if n_q == 0:
         return
     a = bc_kv8_attention_args(q.data_ptr(), out.data_ptr(), dt, q.stride(0) if n_q > 1 else Hq * hd, n_q,

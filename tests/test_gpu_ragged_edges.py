@@ -266,6 +266,16 @@ def test_value_scales_that_outweigh_the_logits(code, dtype, swap):
         assert (np.abs(got / want - 1) <= rel).all(), (D, low, high, float((got / want).min()))
 
 
+@pytest.mark.parametrize("cap", [1e-50, -1e-50, 1e-39])
+def test_attention_refuses_a_cap_that_is_none_in_32_bits(cap):
+    pool, q = to(DEV, make_pool(2, 1, 64, "e4m3", seed=1)), torch.zeros(1, 1, 64, device=DEV)
+    out = torch.full_like(q, 7.0)
+    scratch = torch.zeros(bc.bc_kv8_attention_scratch_bytes(1, 1, 1, 1, 64), dtype=torch.uint8, device=DEV)
+    with pytest.raises(ValueError, match="cap"):
+        bc.kv8_attention(q, pool, ints([20]), ints([[0, 1]]), out, scratch, "e4m3", cap=cap)
+    assert (out == 7).all()
+
+
 # ------------------------------------------------------------------ logits
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_repetition_over_its_range(dtype):
