@@ -11,8 +11,10 @@
 // never meet: old entries are read, new ones written, and the page of a new
 // token is taken from the free list, not from the table.  Only lens_out and
 // n_free_out may lie on inputs; the last CTA to finish (an atomic ticket, no
-// spinning) writes them.  Latency bounds it: 4.3 us for 24 requests that take a
-// token each, 10.6 us for 1000 that take 190 thousand.
+// spinning) writes them.  Graph replays: 4.2 us for 24 requests that take a token
+// each, the latency of a launch and three sums; 10.9 us for 1000 that take 190
+// thousand, 3.9 million warp instructions (half the issue slots), most of them the
+// ten steps of a search for every token and the sums, which every CTA repeats.
 #include "common.cuh"
 #include "entry.h"
 

@@ -10,9 +10,13 @@
 // permutes, and the lane's words are contiguous (16 bytes a group of tokens).
 // HBM bounds both for prompts, the chain slots - tokens - scale - codes a
 // decode step.  A CTA takes a window of tokens and a group of heads; its
-// warps share the items of the runs that begin there.  32768 tokens of 8 heads
-// of 128 are read back in 36 us (5.6 TB/s), 23 thousand appended from bf16 in
-// 29 us (4.8 TB/s); persistent CTAs needed more registers and were slower.
+// warps share the items of the runs that begin there.  Graph replays, 8 heads of
+// 128: 32768 tokens read back as bf16 in 36 us (5.6 TB/s), 23 thousand appended
+// from bf16 in 29 us (4.9 TB/s), from f32 in 41 us (5.7 TB/s); 256 tokens to as
+// many pages 6.6 us.  80 registers a thread, for three CTAs an SM, spill a few
+// words: 60 bytes in the append of f32 at head_dim 128, 4 to 20 in its other
+// forms and in the read-back there, none at 64.  Persistent CTAs spilled more and
+// were slower.
 #include "entry.h"
 #include "kv8.cuh"
 

@@ -5,9 +5,12 @@
 // in one pass over the cache: running maximum m and sum l (base 2), o
 // rescaled as the maximum grows.  Up to 64 query rows of a kv head share the
 // bytes of its pages: up to 8 rows are 32 flops a byte, so HBM bounds them (64
-// sequences of 1K to 8K tokens, 32 / 8 heads of 128, bf16: 454 MB in 80 us, 5.7
-// TB/s, 7.1 while it streams); beyond, instructions do (16 sequences with 1 to
-// 4 drafts of 4 rows, cap and window 4096: 111 MB in 45 us).
+// sequences of 1K to 8K tokens, 32 / 8 heads of 128, bf16: 454 MB in 78.6 us, 5.8
+// TB/s, 7.1 while it streams); beyond, the work of a page and 8 rows does, one
+// chain from its scores to its products on 3 warps a scheduler (16 sequences with
+// 1 to 4 drafts of 4 rows, cap and window 4096: 111 MB in 44.6 us, half of the
+// issue slots, 12% of the tensor pipe).  Times here are of graph replays; a call
+// from Python takes 2 to 4 us more.
 //
 // Work split.  A segment is the pages of one (sequence, kv head, 8 query
 // rows); the pages of all segments, in that order, are one line of units; it
@@ -16,12 +19,12 @@
 // SM) has 12 warps.  A warp reads its pages through a ring in shared memory,
 // filled by bulk copies (a block of a page and head, scales included, is
 // contiguous) 2 pages ahead, 24 blocks per SM (32 only lengthen the
-// queues: 84 against 80 us for 64 sequences of 1K to 8K tokens); the page numbers come from
-// registers, 64 units ahead.  Sequences with more than 8 rows (several
+// queues: 4 us more for 64 sequences of 1K to 8K tokens); the page numbers come
+// from registers, 64 units ahead.  Sequences with more than 8 rows (several
 // queries, or drafts) have their blocks read once per 8 rows, mostly from L2;
 // the products, not the bytes, bound those (sharing a block between the warps
-// of a sequence's rows left warps idle where sequences differ in queries:
-// 55 us for 16 sequences with 1 to 4 drafts in a window of 4096 tokens).
+// of a sequence's rows left warps idle where sequences differ in queries: 11 us
+// more for 16 sequences with 1 to 4 drafts in a window of 4096 tokens).
 // A segment that lies in one warp's piece goes straight to the output.
 // Pieces of a segment are merged in shared memory within a CTA, and through
 // the scratch between CTAs, by the last of them to finish (an atomic ticket
@@ -34,7 +37,9 @@
 // would be 7/8 empty.  A row of q is scaled by a power of two so that its
 // largest element is in [2^14, 2^15).  A bf16 q is exact in f16 (elements below
 // 2^-31 of the largest: to 2^-39 of it), and weights of 11 bits serve a bf16
-// output of 8; for f32 both are split in two f16 numbers, hi + lo (22 bits, or
+// output of 8 (a tenth of the outputs round to a neighbour of the nearest bf16
+// number, with the error against 64 bits that 32-bit weights give, 1.7e-3 in the
+// root mean square of the two cases above); for f32 both are split in two f16 numbers, hi + lo (22 bits, or
 // as many as the smallest f16 number, 2^-24, leaves), for twice the products.
 // The key scale multiplies the logit.  The value scale v of a page enters the
 // weight, w = 2^(x + log2 v - mo + lift), with a second reference mo for x +
@@ -42,8 +47,8 @@
 // seen, however far apart the scales are.  The references m and mo follow
 // the maxima only when one is passed by more than 2^slack (one vote a page): the
 // reductions over the lanes and the rescaling of o leave the usual path.  With
-// slack 2 (f32) they do so a little more often than with 8, 0.2 us of 52.7 for
-// four sequences of 16K to 128K tokens at half the pages.
+// slack 2 (f32) they do so a little more often than with 8: 0.2 us for four
+// sequences of 16K to 128K tokens at half the pages (53.7 us).
 //
 // Fragment order.  Lane (g, t) = (lane / 4, lane % 4).  Dims are contracted
 // in the order in which a lane finds them, 64u + 16t + 4w + 0..3 for step
@@ -630,7 +635,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) k_kv8_attn(const __grid_constan
         // piece is low by up to 2^-24 a page, nothing to bf16 outputs (a tenth of
         // a rounding at 8192 pages) but 1.8e-4 at 4096 pages to f32 ones, whose
         // pages are therefore added to nearest (6e-6; 82.7 against 79.7 us for 64
-        // f32 sequences of 1K to 8K tokens, 53.4 against 52.9 for page lists).
+        // f32 sequences of 1K to 8K tokens, 53.4 against 52.9 for four of 16K to
+        // 128K at half the pages).
         if (SPLIT) {
           float part[4] = {0.f, 0.f, 0.f, 0.f};
           mma_words(part, p, q, ph);

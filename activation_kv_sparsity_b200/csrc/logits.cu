@@ -11,11 +11,11 @@
 // prompt", and the count of the output tokens; a word of the biases the place of
 // the last entry for the id (a maximum), so no result depends on the order of
 // the atomics.
-// 160 rows of 128256 f32 logits with histories of up to 8192 tokens, 32 biases
-// and masks take 41 us (4.0 TB/s of logits), 34 us with histories of up to 1000
-// tokens, 29 us with neither lists nor masks (5.7 TB/s, the copy's rate); in
-// bf16 36, 27 and 17 us.  What the lists cost is the walks and the barriers
-// around them.  Slower were a CTA a piece that walks the lists in L2 (68 us) and a
+// Graph replays: 160 rows of 128256 f32 logits with histories of up to 8192
+// tokens, 32 biases and masks take 41 us (4.0 TB/s of logits), 34 us with
+// histories of up to 1000 tokens, 27 us with neither lists nor masks (6.0 TB/s,
+// the copy's rate); in bf16 36, 28 and 12 us.  What the lists cost is the walks
+// and the barriers around them: every piece of a row walks all of its lists.  Slower were a CTA a piece that walks the lists in L2 (68 us) and a
 // copy and a scatter from hash tables (55); pieces in shared memory by
 // asynchronous copies leave the lists too little room, and cutting a row's list to
 // the CTA's own ids takes longer than the walks that it shortens.
@@ -175,7 +175,9 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas) k_logits(const __gr
       b1 = max(b0, a.bias_ids ? clamp_at(a.bias_start[row + 1], a.n_bias) : 0);
       out0 = h0 + min(a.prompt_len ? max(a.prompt_len[row], 0) : 0, h1 - h0);       // behind the prompt
       rep = a.repetition ? a.repetition[row] : 1.f;
-      inv_rep = __frcp_rn(rep);                 // x / rep to within an ulp and a half, for one multiplication an id
+      // x / rep to within an ulp and a half, for one multiplication an id (41.1 us;
+      // a division where the reciprocal is not a normal number: 42.9)
+      inv_rep = __frcp_rn(rep);
       freq = a.frequency ? a.frequency[row] : 0.f;
       pres = a.presence ? a.presence[row] : 0.f;
       mask = mask_of(a, row);
